@@ -285,6 +285,89 @@ int moe_router_fused_fwd_sort(const mr_router_params* p, const void* logits, int
                               int32_t* num_tokens_post_pad, void* workspace, size_t ws_bytes,
                               int32_t* status, mr_stream_t stream);
 
+/*
+ * ---- The layer behind the router: experts' products and adapter projections ----
+ *
+ * Activations and weights are bf16, products are accumulated in fp32. Any sizes and
+ * any alignment of the element type are accepted: rows that are multiples of 16 bytes
+ * at 16-byte aligned bases (H, I, K and rank multiples of 8) take the tensor-core
+ * path, anything else a plain one (the same results to within rounding, slower).
+ */
+typedef enum { MR_SILU = 0, MR_GELU = 1 } mr_act; /* GELU: x * Phi(x), with the error function */
+
+/*
+ * Expert options.
+ *   T      tokens, >= 0 (T == 0 is a no-op)
+ *   H      hidden size, 1..MR_MAX_WIDTH;  I  intermediate size, 1..MR_MAX_WIDTH
+ *   E      experts that have weights (routed, then shared), 1..MR_MAX_SORT_EXPERTS
+ *   topk   slots per token
+ *   dtype  of x, w13, w2 and out: MR_BF16 (others MR_EUNSUPPORTED)
+ *   act    MR_SILU or MR_GELU
+ */
+#define MR_MAX_WIDTH (1 << 20)
+typedef struct {
+    int32_t T, H, I, E, topk, dtype, act;
+} mr_expert_params;
+
+/*
+ * moe_experts_fwd -- the experts' products for a given choice of experts ([GEMM]
+ * moe_gemm_2stage, the consumer of the sorted layout; the sort runs inside).
+ *   for each token t and slot j with e = topk_idx[t][j] in [0, E):
+ *     g = w13[e][0:I] x[t],  u = w13[e][I:2I] x[t],  h = act(g) * u  (rounded to bf16)
+ *     out[t] = sum_j topk_w[t][j] * (w2[e] h_j)      (fp32, slots in ascending j)
+ * x [T x H], topk_idx int32 [T x topk], topk_w fp32 [T x topk], w13 [E x 2I x H] (gate
+ * rows, then up rows), w2 [E x H x I], out [T x H]. out must not overlap an input.
+ * Slots whose id is outside [0, E) contribute nothing (a token of such slots alone gets a
+ * row of zeros) and raise *status to MR_ERANGE, as in moe_sort. The same expert may
+ * appear in several slots of a token. Results do not depend on the launch: the same
+ * inputs give the same bits.
+ * workspace: device scratch of at least moe_experts_workspace_bytes(), 256-byte aligned,
+ * contents ignored on entry; calls that share one must not overlap on the GPU (two
+ * captured graphs that share one must not run at the same time).
+ * status: nullable device int32 (MR_ERANGE; MR_ETIMEOUT when a bounded wait inside a
+ * kernel gave up, into the library's per-device word when status is NULL).
+ * Errors: MR_EINVAL (null pointer, size out of range, T*topk >= INT_MAX, workspace too
+ * small or misaligned, pointers not aligned to their elements), MR_EUNSUPPORTED (dtype,
+ * E above MR_MAX_SORT_EXPERTS, H or I above MR_MAX_WIDTH), MR_ECUDA.
+ */
+size_t moe_experts_workspace_bytes(const mr_expert_params* p);
+int moe_experts_fwd(const mr_expert_params* p, const void* x, const int32_t* topk_idx, const float* topk_w,
+                    const void* w13, const void* w2, void* out, void* workspace, size_t ws_bytes,
+                    int32_t* status, mr_stream_t stream);
+
+/*
+ * moe_layer_fwd -- the whole layer from the router's logits: moe_router_fwd (compact
+ * outputs) followed by moe_experts_fwd over E_tot = E + n_shared experts, in as few
+ * launches as the sizes allow. p: the routing options; H, I, act: as above, with
+ * E_tot experts in w13 / w2 (the shared experts last). topk_idx / topk_w: nullable
+ * outputs. x and out are bf16; logits as p->in_dtype says. Errors: those of both parts.
+ */
+size_t moe_layer_workspace_bytes(const mr_router_params* p, int H, int I, int act);
+int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* x, const void* logits,
+                  const void* w13, const void* w2, void* out, int32_t* topk_idx, float* topk_w,
+                  void* workspace, size_t ws_bytes, int32_t* status, mr_stream_t stream);
+
+/*
+ * moe_adapter_proj_fwd -- a projection shared by all tokens with the low-rank adapter that
+ * each token's request names (a top-1 choice of weights made by the request instead of
+ * the router), e.g. the router's own projection (hidden state -> logits):
+ *   out[t] = w x[t] + scale[a] * b[a] (a_[a] x[t]),  a = adapter[t];  a < 0: out[t] = w x[t]
+ * x [T x K], w [N x K], a [n_adapters x rank x K], b [n_adapters x N x rank] bf16; adapter
+ * int32 [T]; scale fp32 [n_adapters] (nullable: 1); out [T x N] bf16 or fp32 (out_dtype).
+ * Smaller ranks share a call by padding a's rows or b's columns with zeros. The rank-
+ * space values are kept to 16 significant bits, sums in fp32. adapter[t] >= n_adapters
+ * counts as none and raises *status to MR_ERANGE. n_adapters 0: no adapters (a, b,
+ * scale, adapter ignored). out must not overlap an input.
+ * Limits: K, N, rank 1..MR_MAX_WIDTH, n_adapters >= 0. Workspace, status and errors as above.
+ */
+typedef struct {
+    int32_t T, K, N, n_adapters, rank, dtype, out_dtype;
+} mr_adapter_params;
+size_t moe_adapter_proj_workspace_bytes(const mr_adapter_params* p);
+int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* w, const void* a, const void* b,
+                         const int32_t* adapter, const float* scale, void* out, void* workspace,
+                         size_t ws_bytes, int32_t* status, mr_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* moe_router_strerror(int code);
 

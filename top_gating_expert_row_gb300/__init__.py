@@ -25,6 +25,7 @@ LIB_PATH = os.path.join(_HERE, "libmoerouter.so")
 MR_OK, MR_EINVAL, MR_EUNSUPPORTED, MR_ECUDA, MR_ERANGE, MR_ETIMEOUT = 0, 1, 2, 3, 4, 5
 MR_SOFTMAX, MR_SIGMOID = 0, 1
 MR_F32, MR_BF16 = 0, 1
+MR_SILU, MR_GELU = 0, 1
 MR_MAX_FUSED_TOKENS = 16
 MR_MAX_FUSED_EXPERTS = 1024
 MR_MAX_FUSED_TOKENS_SMALL_E = 64
@@ -40,10 +41,20 @@ class mr_router_params(ctypes.Structure):
                 ("bias", ctypes.c_void_p)]
 
 
+class mr_expert_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "E", "topk", "dtype", "act")]
+
+
+class mr_adapter_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "n_adapters", "rank", "dtype", "out_dtype")]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _PP = ctypes.POINTER(mr_router_params)
+_PE = ctypes.POINTER(mr_expert_params)
+_PA = ctypes.POINTER(mr_adapter_params)
 _SIGS = {
     "moe_router_fwd": ([_PP, _P, _P, _P, _P, _P, _P, _P, _P], _I),
     "moe_router_bwd": ([_PP, _P, _P, _P, _P, _P], _I),
@@ -58,6 +69,12 @@ _SIGS = {
     "moe_router_set_launch_overlap": ([_I], _I),
     "moe_router_fused_workspace_bytes": ([_PP, _I], _SZ),
     "moe_router_fused_fwd_sort": ([_PP, _P, _I, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I),
+    "moe_experts_workspace_bytes": ([_PE], _SZ),
+    "moe_experts_fwd": ([_PE, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I),
+    "moe_layer_workspace_bytes": ([_PP, _I, _I, _I], _SZ),
+    "moe_layer_fwd": ([_PP, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I),
+    "moe_adapter_proj_workspace_bytes": ([_PA], _SZ),
+    "moe_adapter_proj_fwd": ([_PA, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I),
     "moe_router_strerror": ([_I], ctypes.c_char_p),
     "moe_router_set_topk_path": ([_I, _I], _I),
     "moe_router_expf": ([_P, _P, _I, _P], _I),
@@ -307,6 +324,47 @@ def moe_aux_loss_bwd(T, E, topk, coeff, total_num_tokens, tokens_per_expert, gra
                                      _ptr(grad_loss), _ptr(grad_probs), _stream(stream)), "moe_aux_loss_bwd")
 
 
+def moe_experts_workspace_bytes(p: mr_expert_params) -> int:
+    return int(_lib.moe_experts_workspace_bytes(ctypes.byref(p)))
+
+
+def moe_experts_fwd(p: mr_expert_params, x, topk_idx, topk_w, w13, w2, out, workspace, ws_bytes=None, status=None,
+                    stream=None) -> int:
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _ok(_lib.moe_experts_fwd(ctypes.byref(p), _ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(w13), _ptr(w2),
+                                    _ptr(out), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)),
+               "moe_experts_fwd")
+
+
+def moe_layer_workspace_bytes(p, H: int, I: int, act: int = MR_SILU) -> int:
+    cp = _params(p)
+    return int(_lib.moe_layer_workspace_bytes(ctypes.byref(cp), H, I, act))
+
+
+def moe_layer_fwd(p, H, I, act, x, logits, w13, w2, out, topk_idx=None, topk_w=None, workspace=None, ws_bytes=None,
+                  status=None, stream=None) -> int:
+    cp = _params(p)
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _ok(_lib.moe_layer_fwd(ctypes.byref(cp), H, I, act, _ptr(x), _ptr(logits), _ptr(w13), _ptr(w2), _ptr(out),
+                                  _ptr(topk_idx), _ptr(topk_w), _ptr(workspace), ws_bytes, _ptr(status),
+                                  _stream(stream)), "moe_layer_fwd")
+
+
+def moe_adapter_proj_workspace_bytes(p: mr_adapter_params) -> int:
+    return int(_lib.moe_adapter_proj_workspace_bytes(ctypes.byref(p)))
+
+
+def moe_adapter_proj_fwd(p: mr_adapter_params, x, w, a, b, adapter, scale, out, workspace, ws_bytes=None, status=None,
+                         stream=None) -> int:
+    if ws_bytes is None:
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _ok(_lib.moe_adapter_proj_fwd(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(adapter),
+                                         _ptr(scale), _ptr(out), _ptr(workspace), ws_bytes, _ptr(status),
+                                         _stream(stream)), "moe_adapter_proj_fwd")
+
+
 # ------------------------------------------------------------------- allocating helpers
 
 PATH_AUTO, PATH_ARGMAX, PATH_SELECT = 0, 1, 2
@@ -443,3 +501,123 @@ def aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor, T: in
     g = torch.empty(T, E, dtype=torch.float32, device=tokens_per_expert.device)
     moe_aux_loss_bwd(T, E, topk, coeff, N, tokens_per_expert, grad_loss, g, stream)
     return g
+
+
+# ------------------------------------------------------------------- the layer behind the router
+
+
+def _check(what: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, x on {device}")
+
+
+class _Launch:
+    """The device of x made current, and on it `stream` (default: that device's current stream), on which the
+    call's tensors are allocated, so that a workspace is not reused before the call's kernels are done."""
+
+    __slots__ = ("device", "stream")
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError(f"x must be on a CUDA device, got {device}")
+        self.device = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, x on {device}")
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _weights_shape(x, w13, w2):
+    if x.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("x is [T, H], w13 [E, 2*I, H], w2 [E, H, I]")
+    E, I = w13.shape[0], w2.shape[2]
+    H = x.shape[1]
+    _check("x", x, x.shape, torch.bfloat16, x.device)
+    _check("w13", w13, (E, 2 * I, H), torch.bfloat16, x.device)
+    _check("w2", w2, (E, H, I), torch.bfloat16, x.device)
+    return E, H, I
+
+
+def experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
+            act: int = MR_SILU, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_experts_fwd with a freshly allocated output and workspace: out [T, H] (bf16) of x [T, H] (bf16) through
+    the experts topk_idx [T, topk] (int32; ids outside [0, E) are skipped) with weights topk_w (fp32).
+    w13 [E, 2*I, H] holds each expert's gate rows, then its up rows; w2 is [E, H, I]."""
+    E, H, I = _weights_shape(x, w13, w2)
+    T, k = topk_idx.shape if topk_idx.dim() == 2 else (-1, -1)
+    _check("topk_idx", topk_idx, (x.shape[0], k), torch.int32, x.device)
+    _check("topk_w", topk_w, (T, k), torch.float32, x.device)
+    p = mr_expert_params(T, H, I, E, k, MR_BF16, act)
+    with _Launch(x.device, stream):
+        out = torch.empty_like(x)
+        ws = torch.empty(max(1, moe_experts_workspace_bytes(p)), dtype=torch.uint8, device=x.device)
+        moe_experts_fwd(p, x, topk_idx, topk_w, w13, w2, out, ws, None, status)
+    return out
+
+
+def layer(x: torch.Tensor, logits: torch.Tensor, topk: int, w13: torch.Tensor, w2: torch.Tensor, act: int = MR_SILU,
+          status: Optional[torch.Tensor] = None, stream=None, **kw) -> dict:
+    """moe_layer_fwd with freshly allocated outputs: the layer's out [T, H] and the routing it took (topk_idx,
+    topk_w) from x [T, H] (bf16) and router logits [T, E] (fp32 or bf16). Routing options (score_fn, renorm,
+    n_shared, ...) as for route(); w13 / w2 as for experts(), with the shared experts last."""
+    E_tot, H, I = _weights_shape(x, w13, w2)
+    p = params_for(logits, topk, **kw)
+    _check("logits", logits, (x.shape[0], E_tot - p.n_shared), logits.dtype, x.device)
+    cp = p.c()
+    with _Launch(x.device, stream):
+        out = torch.empty_like(x)
+        idx = torch.empty(p.T, topk, dtype=torch.int32, device=x.device)
+        w = torch.empty(p.T, topk, dtype=torch.float32, device=x.device)
+        ws = torch.empty(max(1, moe_layer_workspace_bytes(cp, H, I, act)), dtype=torch.uint8, device=x.device)
+        moe_layer_fwd(cp, H, I, act, x, logits, w13, w2, out, idx, w, ws, None, status)
+    return dict(out=out, topk_idx=idx, topk_w=w)
+
+
+def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = None,
+                 b: Optional[torch.Tensor] = None, adapter: Optional[torch.Tensor] = None,
+                 scale: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                 status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_adapter_proj_fwd with a freshly allocated output: x [T, K] through the shared w [N, K], plus for each
+    token its adapter's scale[i] * b[i] (a[i] x), i = adapter[t] (int32 [T]; negative: none), a [n, rank, K],
+    b [n, N, rank]; out [T, N] in out_dtype (bf16 or fp32). Without a, b, adapter: the projection alone."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x is [T, K], w [N, K]")
+    (T, K), N, dev = x.shape, w.shape[0], x.device
+    _check("x", x, (T, K), torch.bfloat16, dev)
+    _check("w", w, (N, K), torch.bfloat16, dev)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    n = rank = 0
+    if a is not None or b is not None or adapter is not None:
+        if a is None or b is None or adapter is None:
+            raise ValueError("a, b and adapter come together")
+        n, rank = a.shape[:2] if a.dim() == 3 else (-1, -1)
+        _check("a", a, (n, rank, K), torch.bfloat16, dev)
+        _check("b", b, (n, N, rank), torch.bfloat16, dev)
+        _check("adapter", adapter, (T,), torch.int32, dev)
+        if scale is not None:
+            _check("scale", scale, (n,), torch.float32, dev)
+    p = mr_adapter_params(T, K, N, n, rank, MR_BF16, MR_F32 if out_dtype == torch.float32 else MR_BF16)
+    with _Launch(dev, stream):
+        out = torch.empty(T, N, dtype=out_dtype, device=dev)
+        nb = moe_adapter_proj_workspace_bytes(p)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        moe_adapter_proj_fwd(p, x, w, a, b, adapter, scale, out, ws, nb, status)
+    return out

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "moe_router.h"
+#include "experts.h"
 #include "internal.h"
 
 namespace mr {
@@ -458,6 +459,8 @@ int check_sort(int T, int topk, int E_tot, int block_m)
     return MR_OK;
 }
 }  // namespace
+
+int router_check(const mr_router_params* p) { return check_router(p); }
 
 // ---- allocation-free sort: scratch in a file-scope device array ----------------------------------
 

@@ -1,0 +1,322 @@
+// The layer behind the router: argument checks, path choice and launches of
+// moe_experts_fwd, moe_layer_fwd and moe_adapter_proj_fwd, and their plain
+// kernels (any size, any alignment).
+#include <climits>
+#include <cstring>
+
+#include "moe_router.h"
+#include "experts.h"
+
+namespace mr {
+
+// ---------------------------------------------------------------------------
+// Plain kernels: a warp per output element, lanes over the summed index, fp32
+// sums (each lane's in ascending order, then a fixed tree), no shared memory
+// and no alignment beyond the element's. They serve rows that the tensor-core
+// kernels' 16-byte copies cannot address.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float bf(const __nv_bfloat16* p)
+{
+    return bf16_bits_to_f32(__ldcg(reinterpret_cast<const unsigned short*>(p)));
+}
+
+__device__ __forceinline__ float warp_dot(const __nv_bfloat16* a, const __nv_bfloat16* b, int n, int lane)
+{
+    float s = 0.0f;
+    for (int i = lane; i < n; i += 32) s = fmaf(bf(a + i), bf(b + i), s);
+    return warp_sum(s);
+}
+
+// h[pair][i] = act(w13[e][i] . x[t]) * (w13[e][I + i] . x[t]); pairs without an expert are left out
+__global__ void k_experts_up_plain(const __nv_bfloat16* x, const int32_t* idx, const __nv_bfloat16* w13,
+                                   __nv_bfloat16* h, long long P, int topk, int H, int I, int E, int act,
+                                   int32_t* status)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+    for (long long u = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < P * I;
+         u += warps) {
+        const long long pair = u / I;
+        const int i = static_cast<int>(u - pair * I);
+        const int e = __ldcg(idx + pair);
+        if (e < 0 || e >= E) {
+            if (i == 0 && lane == 0) report_status(status, kStatusRange);
+            continue;
+        }
+        const __nv_bfloat16* row = x + pair / topk * H;
+        const __nv_bfloat16* w = w13 + (static_cast<long long>(e) * 2 * I + i) * H;
+        const float g = warp_dot(w, row, H, lane);
+        const float v = warp_dot(w + static_cast<long long>(I) * H, row, H, lane);
+        if (lane == 0) h[u] = __float2bfloat16_rn(act_f32(g, act) * v);
+    }
+}
+
+// out[t][c] = sum_j weight[t][j] * (w2[e_j][c] . h[t][j])
+__global__ void k_experts_down_plain(const __nv_bfloat16* h, const int32_t* idx, const float* weight,
+                                     const __nv_bfloat16* w2, __nv_bfloat16* out, long long T, int topk, int H, int I,
+                                     int E)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+    for (long long u = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < T * H;
+         u += warps) {
+        const long long t = u / H;
+        const int c = static_cast<int>(u - t * H);
+        float acc = 0.0f;
+        for (int j = 0; j < topk; ++j) {
+            const long long pair = t * topk + j;
+            const int e = __ldcg(idx + pair);
+            if (e < 0 || e >= E) continue;
+            const float y = warp_dot(w2 + (static_cast<long long>(e) * H + c) * I, h + pair * I, I, lane);
+            acc = fmaf(__ldcg(weight + pair), y, acc);
+        }
+        if (lane == 0) out[u] = __float2bfloat16_rn(acc);
+    }
+}
+
+// s[t][q] = scale * (a[adapter][q] . x[t])
+__global__ void k_adapter_low_plain(const __nv_bfloat16* x, const __nv_bfloat16* a, const int32_t* adapter,
+                                    const float* scale, float* s, long long T, int K, int rank, int n_adapters,
+                                    int32_t* status)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+    for (long long u = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < T * rank;
+         u += warps) {
+        const long long t = u / rank;
+        const int q = static_cast<int>(u - t * rank);
+        const int ad = __ldcg(adapter + t);
+        if (ad >= n_adapters && q == 0 && lane == 0) report_status(status, kStatusRange);
+        if (ad < 0 || ad >= n_adapters) continue;
+        const float d = warp_dot(a + (static_cast<long long>(ad) * rank + q) * K, x + t * K, K, lane);
+        if (lane == 0) s[u] = scale ? d * __ldcg(scale + ad) : d;
+    }
+}
+
+template <typename OutT>
+__global__ void k_adapter_proj_plain(const __nv_bfloat16* x, const __nv_bfloat16* w, const __nv_bfloat16* b,
+                                     const int32_t* adapter, const float* s, OutT* out, long long T, int K, int N,
+                                     int rank, int n_adapters)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+    for (long long u = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < T * N;
+         u += warps) {
+        const long long t = u / N;
+        const int c = static_cast<int>(u - t * N);
+        float acc = warp_dot(w + static_cast<long long>(c) * K, x + t * K, K, lane);
+        const int ad = n_adapters > 0 ? __ldcg(adapter + t) : -1;
+        if (ad >= 0 && ad < n_adapters) {
+            const __nv_bfloat16* brow = b + (static_cast<long long>(ad) * N + c) * rank;
+            float v = 0.0f;
+            for (int q = lane; q < rank; q += 32) v = fmaf(bf(brow + q), __ldcg(s + t * rank + q), v);
+            acc += warp_sum(v);
+        }
+        if (lane == 0) store_scalar(out + u, acc);
+    }
+}
+
+namespace {
+
+constexpr int kPlainThreads = 256;
+
+int plain_grid(const void* func, long long warps)
+{
+    return persistent_grid(func, kPlainThreads, 0, (warps + kPlainThreads / 32 - 1) / (kPlainThreads / 32));
+}
+
+int from_cuda(int e) { return e == cudaSuccess ? MR_OK : MR_ECUDA; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int check_experts(const mr_expert_params* p)
+{
+    if (!p) return MR_EINVAL;
+    if (p->T < 0 || p->H < 1 || p->I < 1 || p->E < 1 || p->topk < 1) return MR_EINVAL;
+    if (p->dtype != MR_F32 && p->dtype != MR_BF16) return MR_EINVAL;
+    if (p->act != MR_SILU && p->act != MR_GELU) return MR_EINVAL;
+    if (static_cast<long long>(p->T) * p->topk >= INT_MAX) return MR_EINVAL;
+    if (p->dtype != MR_BF16) return MR_EUNSUPPORTED;
+    if (p->H > MR_MAX_WIDTH || p->I > MR_MAX_WIDTH || p->E > MR_MAX_SORT_EXPERTS) return MR_EUNSUPPORTED;
+    return MR_OK;
+}
+
+// The router's options as expert options (E_tot experts).
+mr_expert_params layer_experts(const mr_router_params* p, int H, int I, int act)
+{
+    mr_expert_params q;
+    q.T = p->T;
+    q.H = H;
+    q.I = I;
+    q.E = p->E + p->n_shared;
+    q.topk = p->topk;
+    q.dtype = MR_BF16;
+    q.act = act;
+    return q;
+}
+
+int check_adapter(const mr_adapter_params* p)
+{
+    if (!p) return MR_EINVAL;
+    if (p->T < 0 || p->K < 1 || p->N < 1 || p->n_adapters < 0 || (p->n_adapters > 0 && p->rank < 1)) return MR_EINVAL;
+    if (p->dtype != MR_F32 && p->dtype != MR_BF16) return MR_EINVAL;
+    if (p->out_dtype != MR_F32 && p->out_dtype != MR_BF16) return MR_EINVAL;
+    if (p->dtype != MR_BF16) return MR_EUNSUPPORTED;
+    if (p->K > MR_MAX_WIDTH || p->N > MR_MAX_WIDTH || (p->n_adapters > 0 && p->rank > MR_MAX_WIDTH))
+        return MR_EUNSUPPORTED;
+    return MR_OK;
+}
+
+// Workspace of the experts' products: offsets of its parts.
+struct ExpertPlan {
+    size_t idx, w, h, bytes;
+};
+
+size_t part(size_t& o, size_t bytes)
+{
+    const size_t at = o;
+    o += (bytes + 255) / 256 * 256;
+    return at;
+}
+
+// compact: room for the routed ids and weights too
+ExpertPlan expert_plan(const mr_expert_params& p, bool compact)
+{
+    const size_t P = static_cast<size_t>(p.T) * p.topk;
+    ExpertPlan w;
+    size_t o = 0;
+    w.idx = part(o, compact ? P * 4 : 0);
+    w.w = part(o, compact ? P * 4 : 0);
+    w.h = part(o, P * p.I * 2);
+    w.bytes = o;
+    return w;
+}
+
+int experts_plain(const mr_expert_params& p, const void* x, const int32_t* idx, const float* w, const void* w13,
+                  const void* w2, void* out, unsigned char* ws, const ExpertPlan& plan, int32_t* status,
+                  cudaStream_t st)
+{
+    using B = __nv_bfloat16;
+    B* h = reinterpret_cast<B*>(ws + plan.h);
+    const long long P = static_cast<long long>(p.T) * p.topk;
+    int g = plain_grid(reinterpret_cast<const void*>(&k_experts_up_plain), P * p.I);
+    if (g < 1) return MR_ECUDA;
+    int e = launch_kernel(k_experts_up_plain, dim3(g), dim3(kPlainThreads), 0, st, 0, static_cast<const B*>(x), idx,
+                          static_cast<const B*>(w13), h, P, p.topk, p.H, p.I, p.E, p.act, status);
+    if (e != cudaSuccess) return MR_ECUDA;
+    g = plain_grid(reinterpret_cast<const void*>(&k_experts_down_plain), static_cast<long long>(p.T) * p.H);
+    if (g < 1) return MR_ECUDA;
+    return from_cuda(launch_kernel(k_experts_down_plain, dim3(g), dim3(kPlainThreads), 0, st, 0,
+                                   static_cast<const B*>(h), idx, w, static_cast<const B*>(w2), static_cast<B*>(out),
+                                   static_cast<long long>(p.T), p.topk, p.H, p.I, p.E));
+}
+
+}  // namespace
+}  // namespace mr
+
+using namespace mr;
+
+extern "C" {
+
+size_t moe_experts_workspace_bytes(const mr_expert_params* p)
+{
+    if (check_experts(p) != MR_OK || p->T == 0) return 0;
+    return expert_plan(*p, false).bytes;
+}
+
+int moe_experts_fwd(const mr_expert_params* p, const void* x, const int32_t* topk_idx, const float* topk_w,
+                    const void* w13, const void* w2, void* out, void* workspace, size_t ws_bytes, int32_t* status,
+                    mr_stream_t stream)
+{
+    const int rc = check_experts(p);
+    if (rc != MR_OK) return rc;
+    if (p->T == 0) return MR_OK;
+    if (!x || !topk_idx || !topk_w || !w13 || !w2 || !out || !workspace) return MR_EINVAL;
+    if (!aligned(x, 2) || !aligned(w13, 2) || !aligned(w2, 2) || !aligned(out, 2)) return MR_EINVAL;
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(status, 4)) return MR_EINVAL;
+    const ExpertPlan plan = expert_plan(*p, false);
+    if (ws_bytes < plan.bytes || !aligned(workspace, 256)) return MR_EINVAL;
+    return experts_plain(*p, x, topk_idx, topk_w, w13, w2, out, static_cast<unsigned char*>(workspace), plan, status,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_layer_workspace_bytes(const mr_router_params* p, int H, int I, int act)
+{
+    if (router_check(p) != MR_OK || p->T == 0 || p->n_shared > MR_MAX_SORT_EXPERTS) return 0;
+    const mr_expert_params q = layer_experts(p, H, I, act);
+    if (check_experts(&q) != MR_OK) return 0;
+    return expert_plan(q, true).bytes;
+}
+
+int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* x, const void* logits,
+                  const void* w13, const void* w2, void* out, int32_t* topk_idx, float* topk_w, void* workspace,
+                  size_t ws_bytes, int32_t* status, mr_stream_t stream)
+{
+    int rc = router_check(p);
+    if (rc != MR_OK) return rc;
+    if (p->n_shared > MR_MAX_SORT_EXPERTS) return MR_EUNSUPPORTED;
+    const mr_expert_params q = layer_experts(p, H, I, act);
+    rc = check_experts(&q);
+    if (rc != MR_OK) return rc;
+    if (p->T == 0) return MR_OK;
+    if (!x || !logits || !w13 || !w2 || !out || !workspace) return MR_EINVAL;
+    if (!aligned(x, 2) || !aligned(w13, 2) || !aligned(w2, 2) || !aligned(out, 2)) return MR_EINVAL;
+    if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(status, 4)) return MR_EINVAL;
+    if (!aligned(logits, p->in_dtype == MR_BF16 ? 2 : 4)) return MR_EINVAL;
+    const ExpertPlan plan = expert_plan(q, true);
+    if (ws_bytes < plan.bytes || !aligned(workspace, 256)) return MR_EINVAL;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    int32_t* idx = topk_idx ? topk_idx : reinterpret_cast<int32_t*>(ws + plan.idx);
+    float* w = topk_w ? topk_w : reinterpret_cast<float*>(ws + plan.w);
+    rc = moe_router_fwd(p, logits, nullptr, nullptr, nullptr, idx, w, status, stream);
+    if (rc != MR_OK) return rc;
+    return experts_plain(q, x, idx, w, w13, w2, out, ws, plan, status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t moe_adapter_proj_workspace_bytes(const mr_adapter_params* p)
+{
+    if (check_adapter(p) != MR_OK || p->T == 0 || p->n_adapters == 0) return 0;
+    return static_cast<size_t>(p->T) * p->rank * 4;
+}
+
+int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* w, const void* a, const void* b,
+                         const int32_t* adapter, const float* scale, void* out, void* workspace, size_t ws_bytes,
+                         int32_t* status, mr_stream_t stream)
+{
+    const int rc = check_adapter(p);
+    if (rc != MR_OK) return rc;
+    if (p->T == 0) return MR_OK;
+    if (!x || !w || !out || !aligned(x, 2) || !aligned(w, 2)) return MR_EINVAL;
+    if (!aligned(out, p->out_dtype == MR_F32 ? 4 : 2) || !aligned(status, 4)) return MR_EINVAL;
+    if (p->n_adapters > 0) {
+        if (!a || !b || !adapter || !aligned(a, 2) || !aligned(b, 2) || !aligned(adapter, 4) || !aligned(scale, 4))
+            return MR_EINVAL;
+        if (!workspace || ws_bytes < moe_adapter_proj_workspace_bytes(p) || !aligned(workspace, 256)) return MR_EINVAL;
+    }
+    using B = __nv_bfloat16;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    float* s = static_cast<float*>(workspace);
+    const long long T = p->T;
+    if (p->n_adapters > 0) {
+        const int g = plain_grid(reinterpret_cast<const void*>(&k_adapter_low_plain), T * p->rank);
+        if (g < 1) return MR_ECUDA;
+        const int e = launch_kernel(k_adapter_low_plain, dim3(g), dim3(kPlainThreads), 0, st, 0,
+                                    static_cast<const B*>(x), static_cast<const B*>(a), adapter, scale, s, T, p->K,
+                                    p->rank, p->n_adapters, status);
+        if (e != cudaSuccess) return MR_ECUDA;
+    }
+    auto go = [&](auto kernel, auto* o) {
+        const int g = plain_grid(reinterpret_cast<const void*>(kernel), T * p->N);
+        if (g < 1) return static_cast<int>(MR_ECUDA);
+        return from_cuda(launch_kernel(kernel, dim3(g), dim3(kPlainThreads), 0, st, 0, static_cast<const B*>(x),
+                                       static_cast<const B*>(w), static_cast<const B*>(b), adapter,
+                                       static_cast<const float*>(s), o, T, p->K, p->N, p->rank, p->n_adapters));
+    };
+    return p->out_dtype == MR_F32 ? go(&k_adapter_proj_plain<float>, static_cast<float*>(out))
+                                  : go(&k_adapter_proj_plain<B>, static_cast<B*>(out));
+}
+
+}  // extern "C"
