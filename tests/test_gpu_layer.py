@@ -148,6 +148,7 @@ LAYERS = [
     (17, 64, 4, 128, 64, {}), (64, 32, 4, 256, 64, dict(score_fn=1, renorm=1, scaling=2.5)),
     (65, 96, 9, 64, 64, dict(score_fn=1, n_group=8, topk_group=4, n_shared=1, renorm=1)),
     (300, 16, 3, 128, 64, dict(n_shared=1, shared_weight=0.5)), (513, 8, 2, 64, 64, dict(renorm=1)),
+    (16, 1024, 1008, 64, 32, dict(n_shared=1000, shared_weight=0.25)),
     (3, 4, 2, 33, 17, dict(renorm=1)), (2, 2304, 36, 64, 32, {}), (6, 37, 3, 128, 64, {}),
 ]
 

@@ -34,6 +34,7 @@ UNITS = [
     ("bwd", "bwd.cu", []),
     ("aux_loss", "aux_loss.cu", []),
     ("experts", "experts.cu", []),
+    ("experts_mma", "experts_mma.cu", []),
     ("api", "api.cu", []),
 ]
 

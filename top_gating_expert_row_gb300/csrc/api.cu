@@ -462,6 +462,15 @@ int check_sort(int T, int topk, int E_tot, int block_m)
 
 int router_check(const mr_router_params* p) { return check_router(p); }
 
+int32_t* status_word(int32_t* status) { return status ? status : device_status_address(); }
+
+void wait_test(uint32_t* tries, int* drop)
+{
+    const unsigned t = g_wait_test.tries.load(std::memory_order_relaxed);
+    *tries = t ? t : kWaitLimit;
+    *drop = g_wait_test.drop.load(std::memory_order_relaxed);
+}
+
 // ---- allocation-free sort: scratch in a file-scope device array ----------------------------------
 
 // Scratch of moe_sort_noalloc: the per-chunk expert-count table that moe_sort

@@ -2,12 +2,43 @@
 // moe_experts_fwd, moe_layer_fwd and moe_adapter_proj_fwd, and their plain
 // kernels (any size, any alignment).
 #include <climits>
-#include <cstring>
+#include <cudaTypedefs.h>
 
-#include "moe_router.h"
+#include <algorithm>
+
 #include "experts.h"
 
 namespace mr {
+
+// cuTensorMapEncodeTiled, from the driver that is loaded (the library itself
+// links no driver); nullptr where there is none.
+static PFN_cuTensorMapEncodeTiled_v12000 encode_function()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        const cudaError_t e =
+            cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f)
+                   : nullptr;
+    }();
+    return fn;
+}
+
+bool encode_map(CUtensorMap* m, const void* base, long long width, long long height, long long planes, int box_h)
+{
+    const auto fn = encode_function();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(height),
+                                static_cast<cuuint64_t>(planes > 0 ? planes : 1)};
+    const cuuint64_t strides[2] = {dims[0] * 2, dims[0] * dims[1] * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_h), 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, steps,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // ---------------------------------------------------------------------------
 // Plain kernels: a warp per output element, lanes over the summed index, fp32
@@ -170,9 +201,11 @@ int check_adapter(const mr_adapter_params* p)
     return MR_OK;
 }
 
-// Workspace of the experts' products: offsets of its parts.
+// Workspace of the experts' products: offsets of its parts. The plain kernels
+// use idx, w and h alone.
 struct ExpertPlan {
-    size_t idx, w, h, bytes;
+    size_t idx, w, h, sids, eids, npp, count, y, sort, sort_bytes, bytes;
+    int nt, cap, rows_up, rows_down, mt_up, mt_down;
 };
 
 size_t part(size_t& o, size_t bytes)
@@ -182,17 +215,103 @@ size_t part(size_t& o, size_t bytes)
     return at;
 }
 
-// compact: room for the routed ids and weights too
-ExpertPlan expert_plan(const mr_expert_params& p, bool compact)
+// Columns (pairs) of a block: twice the mean load of an expert that has any, so
+// that few experts need a second block (which reads their weights again). A
+// product only takes the columns that its block fills, so wide blocks cost
+// shared memory, not time.
+int columns_for(long long P, int E)
+{
+    const long long load = 2 * ((P + std::min<long long>(P, E) - 1) / std::min<long long>(P, E));
+    int nt = 16;
+    while (nt < 256 && nt < load) nt *= 2;
+    return nt;
+}
+
+// Weight rows of a stage: 128, fewer when that leaves SMs without a unit.
+int rows_for(long long blocks, int width, int per_row)
+{
+    int rows = 128;
+    while (rows > 32 && blocks * ((static_cast<long long>(width) * per_row + rows - 1) / rows) < 148) rows /= 2;
+    return rows;
+}
+
+// route: the routing options when the call routes too (room for its outputs and workspace)
+ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
 {
     const size_t P = static_cast<size_t>(p.T) * p.topk;
     ExpertPlan w;
+    w.nt = columns_for(static_cast<long long>(P), p.E);
+    // block sizes down to those whose padded total stays an int
+    while (w.nt > 16 && moe_sort_capacity(p.T, p.topk, p.E, w.nt) >= INT_MAX) w.nt /= 2;
+    const size_t cap = moe_sort_capacity(p.T, p.topk, p.E, w.nt);
+    w.cap = cap < INT_MAX ? static_cast<int>(cap) : -1;
+    const long long blocks = std::max<long long>(std::min<long long>(P, p.E), P / w.nt);
+    w.rows_up = rows_for(blocks, p.I, 2);
+    w.rows_down = rows_for(blocks, p.H, 1);
+    w.mt_up = (p.I + w.rows_up / 2 - 1) / (w.rows_up / 2);
+    w.mt_down = (p.H + w.rows_down - 1) / w.rows_down;
     size_t o = 0;
-    w.idx = part(o, compact ? P * 4 : 0);
-    w.w = part(o, compact ? P * 4 : 0);
-    w.h = part(o, P * p.I * 2);
+    w.idx = part(o, route ? P * 4 : 0);
+    w.w = part(o, route ? P * 4 : 0);
+    w.sids = part(o, cap * 4);
+    w.eids = part(o, (cap / w.nt + 1) * 4);
+    w.npp = part(o, 4);
+    w.count = part(o, static_cast<size_t>(p.T) * w.mt_down * 4);
+    w.sort_bytes = moe_sort_workspace_bytes(p.T, p.topk, p.E, w.nt);
+    if (route) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
+    w.sort = part(o, w.sort_bytes);
+    w.h = part(o, std::max(cap, P) * p.I * 2);
+    w.y = part(o, P * p.H * 4);
     w.bytes = o;
     return w;
+}
+
+// Whether the tensor-core kernels' copies can address these arrays: 16-byte
+// aligned bases and row strides.
+bool tensor_path(const mr_expert_params& p, const ExpertPlan& plan, const void* x, const void* w13, const void* w2)
+{
+    const long long blocks = plan.cap / plan.nt + 1;
+    return plan.cap > 0 && p.H % 8 == 0 && p.I % 8 == 0 && aligned(x, 16) && aligned(w13, 16) && aligned(w2, 16) &&
+           blocks * std::max(plan.mt_up, plan.mt_down) < INT_MAX;
+}
+
+int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx, const float* w, const void* w13,
+                   const void* w2, void* out, unsigned char* ws, const ExpertPlan& plan, int32_t* status,
+                   cudaStream_t st)
+{
+    CUtensorMap map13, mapx, map2, maph;
+    if (!encode_map(&map13, w13, p.H, 2ll * p.I, p.E, plan.rows_up / 2) || !encode_map(&mapx, x, p.H, p.T, 0, 1) ||
+        !encode_map(&map2, w2, p.I, p.H, p.E, plan.rows_down) || !encode_map(&maph, ws + plan.h, p.I, plan.cap, 0, 16))
+        return MR_ECUDA;
+    ExpertArgs a;
+    a.sids = reinterpret_cast<int32_t*>(ws + plan.sids);
+    a.eids = reinterpret_cast<int32_t*>(ws + plan.eids);
+    a.npp = reinterpret_cast<int32_t*>(ws + plan.npp);
+    a.idx = idx;
+    a.w = w;
+    a.h = reinterpret_cast<__nv_bfloat16*>(ws + plan.h);
+    a.y = reinterpret_cast<float*>(ws + plan.y);
+    a.count = reinterpret_cast<int32_t*>(ws + plan.count);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.status = status_word(status);
+    a.T = p.T;
+    a.topk = p.topk;
+    a.H = p.H;
+    a.I = p.I;
+    a.E = p.E;
+    a.P = p.T * p.topk;
+    a.cap = plan.cap;
+    a.act = p.act;
+    a.mt_down = plan.mt_down;
+    wait_test(&a.tries, &a.drop);
+    const long long blocks = plan.cap / plan.nt;
+    a.rows = plan.rows_up;
+    a.mt = plan.mt_up;
+    int e = launch_experts_up(plan.nt, map13, mapx, a, blocks * a.mt, st);
+    if (e != cudaSuccess) return MR_ECUDA;
+    a.rows = plan.rows_down;
+    a.mt = plan.mt_down;
+    return from_cuda(launch_experts_down(plan.nt, map2, maph, a, blocks * a.mt, st));
 }
 
 int experts_plain(const mr_expert_params& p, const void* x, const int32_t* idx, const float* w, const void* w13,
@@ -224,7 +343,7 @@ extern "C" {
 size_t moe_experts_workspace_bytes(const mr_expert_params* p)
 {
     if (check_experts(p) != MR_OK || p->T == 0) return 0;
-    return expert_plan(*p, false).bytes;
+    return expert_plan(*p, nullptr).bytes;
 }
 
 int moe_experts_fwd(const mr_expert_params* p, const void* x, const int32_t* topk_idx, const float* topk_w,
@@ -237,10 +356,17 @@ int moe_experts_fwd(const mr_expert_params* p, const void* x, const int32_t* top
     if (!x || !topk_idx || !topk_w || !w13 || !w2 || !out || !workspace) return MR_EINVAL;
     if (!aligned(x, 2) || !aligned(w13, 2) || !aligned(w2, 2) || !aligned(out, 2)) return MR_EINVAL;
     if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(status, 4)) return MR_EINVAL;
-    const ExpertPlan plan = expert_plan(*p, false);
+    const ExpertPlan plan = expert_plan(*p, nullptr);
     if (ws_bytes < plan.bytes || !aligned(workspace, 256)) return MR_EINVAL;
-    return experts_plain(*p, x, topk_idx, topk_w, w13, w2, out, static_cast<unsigned char*>(workspace), plan, status,
-                         reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    if (!tensor_path(*p, plan, x, w13, w2))
+        return experts_plain(*p, x, topk_idx, topk_w, w13, w2, out, ws, plan, status, st);
+    const int e = moe_sort(topk_idx, nullptr, p->T, p->topk, p->E, plan.nt, reinterpret_cast<int32_t*>(ws + plan.sids),
+                           nullptr, reinterpret_cast<int32_t*>(ws + plan.eids),
+                           reinterpret_cast<int32_t*>(ws + plan.npp), ws + plan.sort, plan.sort_bytes, status, stream);
+    if (e != MR_OK) return e;
+    return experts_tensor(*p, x, topk_idx, topk_w, w13, w2, out, ws, plan, status, st);
 }
 
 size_t moe_layer_workspace_bytes(const mr_router_params* p, int H, int I, int act)
@@ -248,7 +374,7 @@ size_t moe_layer_workspace_bytes(const mr_router_params* p, int H, int I, int ac
     if (router_check(p) != MR_OK || p->T == 0 || p->n_shared > MR_MAX_SORT_EXPERTS) return 0;
     const mr_expert_params q = layer_experts(p, H, I, act);
     if (check_experts(&q) != MR_OK) return 0;
-    return expert_plan(q, true).bytes;
+    return expert_plan(q, p).bytes;
 }
 
 int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* x, const void* logits,
@@ -266,14 +392,29 @@ int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* 
     if (!aligned(x, 2) || !aligned(w13, 2) || !aligned(w2, 2) || !aligned(out, 2)) return MR_EINVAL;
     if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(status, 4)) return MR_EINVAL;
     if (!aligned(logits, p->in_dtype == MR_BF16 ? 2 : 4)) return MR_EINVAL;
-    const ExpertPlan plan = expert_plan(q, true);
+    const ExpertPlan plan = expert_plan(q, p);
     if (ws_bytes < plan.bytes || !aligned(workspace, 256)) return MR_EINVAL;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     int32_t* idx = topk_idx ? topk_idx : reinterpret_cast<int32_t*>(ws + plan.idx);
     float* w = topk_w ? topk_w : reinterpret_cast<float*>(ws + plan.w);
-    rc = moe_router_fwd(p, logits, nullptr, nullptr, nullptr, idx, w, status, stream);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!tensor_path(q, plan, x, w13, w2)) {
+        rc = moe_router_fwd(p, logits, nullptr, nullptr, nullptr, idx, w, status, stream);
+        return rc != MR_OK ? rc : experts_plain(q, x, idx, w, w13, w2, out, ws, plan, status, st);
+    }
+    int32_t* sids = reinterpret_cast<int32_t*>(ws + plan.sids);
+    int32_t* eids = reinterpret_cast<int32_t*>(ws + plan.eids);
+    int32_t* npp = reinterpret_cast<int32_t*>(ws + plan.npp);
+    rc = moe_router_fused_fwd_sort(p, logits, plan.nt, idx, w, sids, nullptr, eids, npp, ws + plan.sort,
+                                   plan.sort_bytes, status, stream);
+    if (rc == MR_EUNSUPPORTED) {  // few tokens with more slots than the one-launch form's shared memory holds
+        rc = moe_router_fwd(p, logits, nullptr, nullptr, nullptr, idx, w, status, stream);
+        if (rc == MR_OK)
+            rc = moe_sort(idx, nullptr, q.T, q.topk, q.E, plan.nt, sids, nullptr, eids, npp, ws + plan.sort,
+                          plan.sort_bytes, status, stream);
+    }
     if (rc != MR_OK) return rc;
-    return experts_plain(q, x, idx, w, w13, w2, out, ws, plan, status, reinterpret_cast<cudaStream_t>(stream));
+    return experts_tensor(q, x, idx, w, w13, w2, out, ws, plan, status, st);
 }
 
 size_t moe_adapter_proj_workspace_bytes(const mr_adapter_params* p)

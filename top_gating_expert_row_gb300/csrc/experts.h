@@ -1,6 +1,8 @@
 // Shared by the translation units of the layer behind the router.
 #pragma once
 
+#include <cuda.h>
+
 #include "internal.h"
 #include "moe_router.h"
 
@@ -12,7 +14,43 @@ __device__ __forceinline__ float act_f32(float g, int act)
     return act == MR_SILU ? g / (1.0f + expf(-g)) : 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
 }
 
-// The validation of the forward calls' options (api.cu).
+// Waits on copies in flight when a CTA gives up (attempts of about a microsecond).
+constexpr uint32_t kDrainTries = 1u << 14;
+
+// What the experts' kernels work on (device pointers; the sorted layout with
+// blocks of nt pairs).
+struct ExpertArgs {
+    const int32_t* sids;   // sorted pair ids, P at sentinels
+    const int32_t* eids;   // expert of each block
+    const int32_t* npp;    // rows of the sorted layout
+    const int32_t* idx;    // [T][topk]
+    const float* w;        // [T][topk]
+    __nv_bfloat16* h;      // [cap][I], in sorted order
+    float* y;              // [T * topk][H], weighted
+    int32_t* count;        // [T][mt_down] slots done
+    __nv_bfloat16* out;    // [T][H]
+    int32_t* status;
+    int T, topk, H, I, E, P, cap;
+    int rows;              // weight rows of a stage (up: gate and up rows together)
+    int mt;                // row tiles of this kernel
+    int mt_down;           // row tiles of `down`
+    int stages, act, drop;
+    uint32_t tries;
+};
+
+int launch_experts_up(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t, const ExpertArgs& a, long long units,
+                      cudaStream_t st);
+int launch_experts_down(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t, const ExpertArgs& a,
+                        long long units, cudaStream_t st);
+
+// A tensor map of bf16 [planes][height][width] (planes 0: a matrix) with boxes
+// of box_h rows by 64 columns, 128-byte swizzled; elements outside read as 0.
+bool encode_map(CUtensorMap* m, const void* base, long long width, long long height, long long planes, int box_h);
+
+// The validation of the forward calls' options, the per-device status word and
+// the wait-test settings (api.cu).
 int router_check(const mr_router_params* p);
+int32_t* status_word(int32_t* status);
+void wait_test(uint32_t* tries, int* drop);
 
 }  // namespace mr
