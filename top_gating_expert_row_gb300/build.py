@@ -1,7 +1,8 @@
 """Build libmoerouter.so for sm_103a with nvcc, in-tree.
 
 Translation units compile in parallel (fwd.cu once per score function x logits
-dtype, plus sort.cu, bwd.cu, aux_loss.cu, experts.cu, api.cu) and link into one shared library with the
+dtype, plus sort.cu, bwd.cu, aux_loss.cu, experts.cu, experts_mma.cu,
+adapter_mma.cu, api.cu) and link into one shared library with the
 static CUDA runtime, so loading it needs no CUDA library path.
 
     python -m top_gating_expert_row_gb300.build [--verbose]
@@ -35,6 +36,7 @@ UNITS = [
     ("aux_loss", "aux_loss.cu", []),
     ("experts", "experts.cu", []),
     ("experts_mma", "experts_mma.cu", []),
+    ("adapter_mma", "adapter_mma.cu", []),
     ("api", "api.cu", []),
 ]
 

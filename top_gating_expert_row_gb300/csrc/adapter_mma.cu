@@ -1,0 +1,560 @@
+// The adapter projection on the tensor cores.
+//
+//   k_adapter_low   s[t] = scale * (a[i] . x_t), the rank-space values of each token's adapter i, as
+//                   partial sums over slices of K
+//   k_adapter_proj  out[t] = w . x_t + b[i] . s[t]
+//
+// Tokens are taken in tiles of at most NT and need no sorting by adapter.
+//
+// The second part of k_adapter_proj, rank multiply-adds an output, is taken by
+// the epilogue warps in fp32 while the tensor cores sum over K: each token's
+// with its own b[i] only. (As further columns of the tensor cores' sum, the
+// tokens of other adapters would meet b[i] with zeros, and an infinity in one
+// request's adapter would reach every token of the tile.)
+//
+// k_adapter_proj starts while k_adapter_low runs (its sum over K needs nothing
+// of it), so the low-rank product costs little time of its own once w is large.
+#include "experts.h"
+#include "gemm.cuh"
+
+namespace mr {
+
+namespace {
+constexpr int kSmallTile = 64;  // tiles up to this keep the adapters' part of a whole unit in shared memory
+
+struct AdapterLayout {
+    uint32_t a, b, ids, list, low, part, bars, bytes;
+};
+}  // namespace
+
+// rank: 0 for a kernel (or call) without the adapters' part. low: rank-space
+// values (small tiles: of all tokens; else of 16, rank-major); part: small
+// tiles: the adapters' part of the unit; else b[i]'s rows of the unit.
+__host__ __device__ inline AdapterLayout adapter_layout(int nt, int rows, int stages, int rank)
+{
+    AdapterLayout L;
+    uint32_t o = 0;
+    L.a = o; o += static_cast<uint32_t>(stages) * rows * kStepBytes;
+    L.b = o; o += static_cast<uint32_t>(stages) * nt * kStepBytes;
+    // a product reads 128 rows from the start of a stage, also of the last one
+    const uint32_t reach = static_cast<uint32_t>(stages - 1) * rows * kStepBytes + 128 * kStepBytes;
+    if (o < reach) o = reach;
+    L.ids = o; o += static_cast<uint32_t>(nt) * 4;
+    L.list = o; o += static_cast<uint32_t>(nt) * 4 + 16;
+    o = (o + 15) / 16 * 16;
+    L.low = o; o += static_cast<uint32_t>(nt <= kSmallTile ? nt : 16) * rank * 4;
+    L.part = o; o += rank == 0 ? 0 : nt <= kSmallTile ? static_cast<uint32_t>(nt) * rows * 4
+                                                      : static_cast<uint32_t>(rows) * (rank + 8) * 2;
+    o = (o + 15) / 16 * 16;
+    L.bars = o; o += sizeof(GemmBars);
+    L.bytes = o + 1024;
+    return L;
+}
+
+// ---- rank-space values -------------------------------------------------------------------------------------------
+
+// A CTA works on one tile of tokens, one slice of K, and every gridDim.z-th
+// group of the tile's distinct adapters; a group is as many adapters as fill
+// the 128 rows of a product.
+template <int NT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    k_adapter_low(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ AdapterArgs a)
+{
+    extern __shared__ unsigned char raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const AdapterLayout L = adapter_layout(NT, 128, a.stages_low, 0);
+    GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
+    int* slot = reinterpret_cast<int*>(smem + L.ids);    // token -> place in the list, -1: none
+    int* list = reinterpret_cast<int*>(smem + L.list);   // the tile's distinct adapters, by first appearance
+    int* count = list + NT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr uint32_t kColumns = 2 * NT;
+    const int group = 128 / a.rank;
+    const uint32_t ring_a = smem_addr(smem + L.a), ring_b = smem_addr(smem + L.b);
+    const int t0 = blockIdx.x * NT, tokens = min(NT, a.T - t0);
+
+    if (warp == 1) tmem_alloc(&bars.tmem, kColumns);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages_low; ++i) {
+            mbar_init(&bars.full[i], 2);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.acc_full[i], 1);
+            mbar_init(&bars.acc_empty[i], kEpilogueThreads);
+        }
+        mbar_init(&bars.drained, 1);
+        bars.gone = 0;
+        *count = 0;
+        prefetch_map(&map_a);
+        prefetch_map(&map_x);
+    }
+    pdl_wait();
+    pdl_trigger();
+    // the distinct adapters of the tile
+    for (int t = threadIdx.x; t < NT; t += kGemmThreads) {
+        const int id = t < tokens ? __ldcg(a.adapter + t0 + t) : -1;
+        if (id >= a.n_adapters && blockIdx.y == 0 && blockIdx.z == 0) report_status(a.range_status, kStatusRange);
+        slot[t] = id >= 0 && id < a.n_adapters ? id : -1;
+    }
+    __syncthreads();
+    int id = -1, first = -1;
+    if (threadIdx.x < NT) {
+        id = slot[threadIdx.x];
+        if (id >= 0) {
+            first = threadIdx.x;
+            for (int t = 0; t < static_cast<int>(threadIdx.x); ++t)
+                if (slot[t] == id) {
+                    first = t;
+                    break;
+                }
+        }
+    }
+    __syncthreads();
+    // the place of a first appearance: how many there are before it
+    if (threadIdx.x < NT) list[threadIdx.x] = first == static_cast<int>(threadIdx.x);
+    __syncthreads();
+    int place = -1;
+    if (first >= 0) {
+        place = 0;
+        for (int t = 0; t < first; ++t) place += list[t];
+    }
+    __syncthreads();
+    if (threadIdx.x < NT) slot[threadIdx.x] = place;
+    if (first == static_cast<int>(threadIdx.x) && id >= 0) {
+        list[place] = id;
+        atomicAdd(count, 1);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    const int distinct = *count;
+
+    const Waits wait{&bars.gone, a.tries};
+    const uint32_t drain = min(a.tries, kDrainTries);
+    const int groups = (distinct + group - 1) / group;
+    const int ksteps = (a.K + kStepK - 1) / kStepK;
+    const int k0 = static_cast<int>(static_cast<long long>(ksteps) * blockIdx.y / gridDim.y);
+    const int k1 = static_cast<int>(static_cast<long long>(ksteps) * (blockIdx.y + 1) / gridDim.y);
+    const int cols = (tokens + 15) & ~15;
+    RingPos pos;
+    int issued = 0;
+    bool ok = true;
+
+    if (warp == 0) {
+        for (int g = blockIdx.z; ok && g < groups; g += gridDim.z) {
+            const int n = min(group, distinct - g * group);
+            for (int k = k0; k < k1; ++k) {
+                ok = __all_sync(kFull, pos.wraps == 0 || wait(&bars.empty[pos.s], (pos.wraps - 1) & 1));
+                if (!ok) break;
+                uint64_t* full = &bars.full[pos.s];
+                if (lane == 0) mbar_expect(full, n * a.rank * kStepBytes);
+                ++issued;
+                __syncwarp();
+                if (lane < n && !a.drop)
+                    load_box3(ring_a + pos.s * (128 * kStepBytes) + lane * a.rank * kStepBytes, &map_a, k * kStepK, 0,
+                              list[g * group + lane], full);
+                pos.next(a.stages_low);
+            }
+        }
+    } else if (warp == 2) {
+        if (lane == 0)
+            for (int g = blockIdx.z; ok && g < groups; g += gridDim.z)
+                for (int k = k0; k < k1; ++k) {
+                    ok = pos.wraps == 0 || wait(&bars.empty[pos.s], (pos.wraps - 1) & 1);
+                    if (!ok) break;
+                    uint64_t* full = &bars.full[pos.s];
+                    mbar_expect(full, NT * kStepBytes);
+                    ++issued;
+                    if (!a.drop) load_box2(ring_b + pos.s * (NT * kStepBytes), &map_x, k * kStepK, t0, full);
+                    pos.next(a.stages_low);
+                }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int seen = 0;
+            const uint32_t desc = product_desc(cols);
+            for (int g = blockIdx.z; ok && g < groups; g += gridDim.z, ++seen) {
+                const int buf = seen & 1;
+                ok = seen < 2 || wait(&bars.acc_empty[buf], ((seen >> 1) - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = k0; k < k1; ++k) {
+                    ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t da = operand_desc(ring_a + pos.s * (128 * kStepBytes));
+                    const uint64_t db = operand_desc(ring_b + pos.s * (NT * kStepBytes));
+#pragma unroll
+                    for (int q = 0; q < kStepK / 16; ++q) mma16(tmem + buf * NT, da + q * 2, db + q * 2, desc, k > k0 || q > 0);
+                    mma_commit(&bars.empty[pos.s]);
+                    pos.next(a.stages_low);
+                }
+                if (ok) mma_commit(&bars.acc_full[buf]);
+            }
+            if (!ok) {
+                mma_commit(&bars.drained);
+                mbar_wait(&bars.drained, 0, drain);
+            }
+        }
+    } else if (warp >= 4) {
+        const int et = threadIdx.x - kEpilogueThreads, q = warp - 4;
+        const int j = et / a.rank, r = et - j * a.rank;
+        float* part = a.low + static_cast<long long>(blockIdx.y) * a.T * a.rank;
+        int seen = 0;
+        for (int g = blockIdx.z; g < groups; g += gridDim.z, ++seen) {
+            const int buf = seen & 1;
+            if (!epilogue_wait(wait, &bars.acc_full[buf], (seen >> 1) & 1)) break;
+            tc_fence_after();
+            const int mine = j < group && g * group + j < distinct ? g * group + j : -2;
+            const float sc = mine < 0 ? 0.0f : (a.scale ? __ldcg(a.scale + list[mine]) : 1.0f);
+            const uint32_t acc = tmem + buf * NT + (static_cast<uint32_t>(q * 32) << 16);
+            for (int c0 = 0; c0 < tokens; c0 += 16) {
+                float v[16];
+                tmem_load16(acc + c0, v);
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    if (c0 + c < tokens && slot[c0 + c] == mine)
+                        part[static_cast<long long>(t0 + c0 + c) * a.rank + r] = v[c] * sc;
+            }
+            tc_fence_before();
+            mbar_arrive(&bars.acc_empty[buf]);
+        }
+    }
+    if ((warp == 0 || warp == 2) && lane == 0 && !ok)
+        for (int s = 0; s < a.stages_low && s < issued; ++s)
+            mbar_wait(&bars.full[s], ((issued - 1 - s) / a.stages_low) & 1, drain);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, kColumns);
+    }
+    if (threadIdx.x == 0 && bars.gone) report_status(a.status, kStatusTimeout);
+}
+
+// ---- projection --------------------------------------------------------------------------------------------------
+
+// Sum over the slices of four rank-space values.
+__device__ __forceinline__ float4 low4(const AdapterArgs& a, long long t, int r)
+{
+    const float* s = a.low + t * a.rank + r;
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int p = 0; p < a.slices; ++p) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(s + static_cast<long long>(p) * a.T * a.rank));
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    return v;
+}
+
+__device__ __forceinline__ void unpack8(uint4 p, float (&v)[8])
+{
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// b[row] . s over the ranks; b in device memory, s fp32 with `step` floats from rank to rank.
+__device__ __forceinline__ float rank_dot(const __nv_bfloat16* brow, const float* s, int step, int rank)
+{
+    float v = 0.0f;
+#pragma unroll 2
+    for (int r = 0; r < rank; r += 8) {
+        float w[8];
+        unpack8(__ldcg(reinterpret_cast<const uint4*>(brow + r)), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v = fmaf(w[i], s[(r + i) * step], v);
+    }
+    return v;
+}
+
+template <int NT, typename OutT>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    k_adapter_proj(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ AdapterArgs a)
+{
+    extern __shared__ unsigned char raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const AdapterLayout L = adapter_layout(NT, a.rows, a.stages, a.n_adapters > 0 ? a.rank : 0);
+    GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr uint32_t kColumns = 2 * NT;
+    const uint32_t a_bytes = a.rows * kStepBytes, b_bytes = NT * kStepBytes;
+    const uint32_t ring_a = smem_addr(smem + L.a), ring_b = smem_addr(smem + L.b);
+
+    if (warp == 1) tmem_alloc(&bars.tmem, kColumns);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(&bars.full[i], 2);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.acc_full[i], 1);
+            mbar_init(&bars.acc_empty[i], kEpilogueThreads);
+        }
+        mbar_init(&bars.drained, 1);
+        bars.gone = 0;
+        prefetch_map(&map_w);
+        prefetch_map(&map_x);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem;
+    // Alone in the call, it follows whatever made x. After k_adapter_low, whose
+    // trigger comes after its own wait, x and w are there already.
+    const bool low = a.n_adapters > 0;
+    if (!low) pdl_wait();
+
+    const Waits wait{&bars.gone, a.tries};
+    const uint32_t drain = min(a.tries, kDrainTries);
+    const int units = a.tiles * a.mt;
+    const int ksteps = (a.K + kStepK - 1) / kStepK;
+    RingPos pos;
+    int issued = 0;
+    bool ok = true;
+
+    if (warp == 0 || warp == 2) {
+        if (lane == 0) {
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const int b = u / a.mt, m = u - b * a.mt;
+                for (int k = 0; k < ksteps; ++k) {
+                    ok = pos.wraps == 0 || wait(&bars.empty[pos.s], (pos.wraps - 1) & 1);
+                    if (!ok) break;
+                    uint64_t* full = &bars.full[pos.s];
+                    mbar_expect(full, warp == 0 ? a_bytes : b_bytes);
+                    ++issued;
+                    if (!a.drop) {
+                        if (warp == 0) load_box2(ring_a + pos.s * a_bytes, &map_w, k * kStepK, m * a.rows, full);
+                        else load_box2(ring_b + pos.s * b_bytes, &map_x, k * kStepK, b * NT, full);
+                    }
+                    pos.next(a.stages);
+                }
+            }
+            if (!ok)
+                for (int s = 0; s < a.stages && s < issued; ++s)
+                    mbar_wait(&bars.full[s], ((issued - 1 - s) / a.stages) & 1, drain);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int seen = 0;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++seen) {
+                const int b = u / a.mt, buf = seen & 1;
+                const uint32_t desc = product_desc((min(NT, a.T - b * NT) + 15) & ~15), d = tmem + buf * NT;
+                ok = seen < 2 || wait(&bars.acc_empty[buf], ((seen >> 1) - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < ksteps; ++k) {
+                    ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t da = operand_desc(ring_a + pos.s * a_bytes), db = operand_desc(ring_b + pos.s * b_bytes);
+#pragma unroll
+                    for (int q = 0; q < kStepK / 16; ++q) mma16(d, da + q * 2, db + q * 2, desc, k > 0 || q > 0);
+                    mma_commit(&bars.empty[pos.s]);
+                    pos.next(a.stages);
+                }
+                if (ok) mma_commit(&bars.acc_full[buf]);
+            }
+            if (!ok) {
+                mma_commit(&bars.drained);
+                mbar_wait(&bars.drained, 0, drain);
+            }
+        }
+    } else if (warp >= 4) {
+        const int et = threadIdx.x - kEpilogueThreads, q = warp - 4;
+        int* mine = reinterpret_cast<int*>(smem + L.ids);      // the tile's adapters, -1: none
+        float* s = reinterpret_cast<float*>(smem + L.low);
+        float* part = reinterpret_cast<float*>(smem + L.part);
+        __nv_bfloat16* rows_b = reinterpret_cast<__nv_bfloat16*>(smem + L.part);
+        const int rank = a.rank, pitch = rank + 8;             // 16 bytes more a row: no bank conflicts
+        if (low) pdl_wait();
+        int seen = 0, tile = -1;
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++seen) {
+            const int b = u / a.mt, m = u - b * a.mt, buf = seen & 1, t0 = b * NT, tokens = min(NT, a.T - t0);
+            const int row = m * a.rows + et;
+            const bool there = et < a.rows && row < a.N;
+            if (low) {
+                epilogue_sync();  // the last unit's values have been read
+                if (b != tile)
+                    for (int t = et; t < NT; t += kEpilogueThreads) {
+                        const int id = t < tokens ? __ldcg(a.adapter + t0 + t) : -1;
+                        mine[t] = id < a.n_adapters ? max(id, -1) : -1;
+                    }
+                if (NT <= kSmallTile) {
+                    epilogue_sync();
+                    if (b != tile)
+                        for (int f = et; f < tokens * (rank >> 2); f += kEpilogueThreads) {
+                            const int t = f / (rank >> 2), r = (f - t * (rank >> 2)) * 4;
+                            if (mine[t] >= 0) *reinterpret_cast<float4*>(s + t * rank + r) = low4(a, t0 + t, r);
+                        }
+                    epilogue_sync();
+                    const int er = et % a.rows, orow = m * a.rows + er;
+                    for (int t = et / a.rows; t < tokens; t += kEpilogueThreads / a.rows)
+                        part[t * a.rows + er] =
+                            mine[t] >= 0 && orow < a.N
+                                ? rank_dot(a.b + (static_cast<long long>(mine[t]) * a.N + orow) * rank, s + t * rank, 1, rank)
+                                : 0.0f;
+                }
+                tile = b;
+            }
+            if (!epilogue_wait(wait, &bars.acc_full[buf], (seen >> 1) & 1)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * NT + (static_cast<uint32_t>(q * 32) << 16);
+            OutT* out = static_cast<OutT*>(a.out) + static_cast<long long>(t0) * a.N + row;
+            int held = -1;  // the adapter whose rows are in rows_b
+            for (int c0 = 0; c0 < tokens; c0 += 16) {
+                float v[16];
+                tmem_load16(acc + c0, v);
+                if (low && NT <= kSmallTile) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (et < a.rows && c0 + c < tokens) v[c] += part[(c0 + c) * a.rows + et];
+                } else if (low) {
+                    const int ad = mine[c0];
+                    bool same = true, any = false;
+                    for (int c = 0; c < 16; ++c) {
+                        same = same && (c0 + c >= tokens || mine[c0 + c] == ad);
+                        any = any || mine[c0 + c] >= 0;
+                    }
+                    if (any) {
+                        epilogue_sync();  // the last 16 tokens' values have been read
+                        for (int f = et; f < 16 * (rank >> 2); f += kEpilogueThreads) {
+                            const int c = f & 15, r = (f >> 4) * 4;
+                            float4 x = make_float4(0, 0, 0, 0);
+                            if (mine[c0 + c] >= 0) x = low4(a, t0 + c0 + c, r);
+                            s[r * 16 + c] = x.x;
+                            s[(r + 1) * 16 + c] = x.y;
+                            s[(r + 2) * 16 + c] = x.z;
+                            s[(r + 3) * 16 + c] = x.w;
+                        }
+                        if (same && ad != held) {
+                            for (int f = et; f < a.rows * (rank >> 3); f += kEpilogueThreads) {
+                                const int i = f / (rank >> 3), r = (f - i * (rank >> 3)) * 8;
+                                if (m * a.rows + i < a.N)
+                                    *reinterpret_cast<uint4*>(rows_b + i * pitch + r) = __ldcg(reinterpret_cast<const uint4*>(
+                                        a.b + (static_cast<long long>(ad) * a.N + m * a.rows + i) * rank + r));
+                            }
+                            held = ad;
+                        }
+                        epilogue_sync();
+                        if (there && same) {
+                            for (int r = 0; r < rank; r += 8) {
+                                float w[8];
+                                unpack8(*reinterpret_cast<const uint4*>(rows_b + et * pitch + r), w);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4* x = reinterpret_cast<const float4*>(s + (r + i) * 16);
+#pragma unroll
+                                    for (int g = 0; g < 4; ++g) {
+                                        const float4 y = x[g];
+                                        const float2 p = __ffma2_rn(make_float2(w[i], w[i]), make_float2(y.x, y.y),
+                                                                    make_float2(v[g * 4], v[g * 4 + 1]));
+                                        const float2 z = __ffma2_rn(make_float2(w[i], w[i]), make_float2(y.z, y.w),
+                                                                    make_float2(v[g * 4 + 2], v[g * 4 + 3]));
+                                        v[g * 4] = p.x;
+                                        v[g * 4 + 1] = p.y;
+                                        v[g * 4 + 2] = z.x;
+                                        v[g * 4 + 3] = z.y;
+                                    }
+                                }
+                            }
+                        } else if (there) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                if (mine[c0 + c] >= 0)
+                                    v[c] += rank_dot(a.b + (static_cast<long long>(mine[c0 + c]) * a.N + row) * rank, s + c,
+                                                     16, rank);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    if (there && c0 + c < tokens) store_scalar(out + static_cast<long long>(c0 + c) * a.N, v[c]);
+            }
+            tc_fence_before();
+            mbar_arrive(&bars.acc_empty[buf]);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, kColumns);
+    }
+    if (threadIdx.x == 0 && bars.gone) report_status(a.status, kStatusTimeout);
+}
+
+namespace {
+
+// k_adapter_proj leaves room for a CTA of k_adapter_low beside it.
+constexpr int kLowBudget = 60 * 1024, kProjBudget = 164 * 1024;
+
+int stages_for(int nt, int rows, int rank, int budget)
+{
+    int s = kMaxStages;
+    while (s > 2 && static_cast<int>(adapter_layout(nt, rows, s, rank).bytes) > budget) --s;
+    return s;
+}
+
+template <int NT>
+int launch_low(const CUtensorMap& map_a, const CUtensorMap& map_x, AdapterArgs a, int groups, cudaStream_t st)
+{
+    a.stages_low = stages_for(NT, 128, 0, kLowBudget);
+    const size_t smem = adapter_layout(NT, 128, a.stages_low, 0).bytes;
+    const int e = ensure_smem(reinterpret_cast<const void*>(&k_adapter_low<NT>), smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(&k_adapter_low<NT>, dim3(a.tiles, a.slices, groups), dim3(kGemmThreads), smem, st, 0, map_a,
+                         map_x, a);
+}
+
+template <int NT, typename OutT>
+int launch_proj(const CUtensorMap& map_w, const CUtensorMap& map_x, AdapterArgs a, cudaStream_t st)
+{
+    const int rank = a.n_adapters > 0 ? a.rank : 0;
+    a.stages = stages_for(NT, a.rows, rank, NT == 256 ? 212 * 1024 : kProjBudget);
+    const size_t smem = adapter_layout(NT, a.rows, a.stages, rank).bytes;
+    const void* f = reinterpret_cast<const void*>(&k_adapter_proj<NT, OutT>);
+    const int e = ensure_smem(f, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = persistent_grid(f, kGemmThreads, smem, static_cast<long long>(a.tiles) * a.mt);
+    if (grid < 1) return cudaErrorLaunchOutOfResources;
+    return launch_kernel(&k_adapter_proj<NT, OutT>, dim3(grid), dim3(kGemmThreads), smem, st, 0, map_w, map_x, a);
+}
+
+}  // namespace
+
+int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_x, const AdapterArgs& a, int groups,
+                       cudaStream_t st)
+{
+    switch (nt) {
+        case 16: return launch_low<16>(map_a, map_x, a, groups, st);
+        case 32: return launch_low<32>(map_a, map_x, a, groups, st);
+        case 64: return launch_low<64>(map_a, map_x, a, groups, st);
+        case 128: return launch_low<128>(map_a, map_x, a, groups, st);
+        default: return launch_low<256>(map_a, map_x, a, groups, st);
+    }
+}
+
+int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const AdapterArgs& a,
+                        cudaStream_t st)
+{
+    auto go = [&](auto f, auto b) { return f32 ? f(map_w, map_x, a, st) : b(map_w, map_x, a, st); };
+    using B = __nv_bfloat16;
+    switch (nt) {
+        case 16: return go(&launch_proj<16, float>, &launch_proj<16, B>);
+        case 32: return go(&launch_proj<32, float>, &launch_proj<32, B>);
+        case 64: return go(&launch_proj<64, float>, &launch_proj<64, B>);
+        case 128: return go(&launch_proj<128, float>, &launch_proj<128, B>);
+        default: return go(&launch_proj<256, float>, &launch_proj<256, B>);
+    }
+}
+
+}  // namespace mr

@@ -314,6 +314,45 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     return from_cuda(launch_experts_down(plan.nt, map2, maph, a, blocks * a.mt, st));
 }
 
+// Workspace of the adapter projection (the rank-space values; the plain kernels
+// use one slice) and its shapes.
+struct AdapterPlan {
+    size_t bytes;
+    int nt, tiles, rows, mt, slices, groups;
+};
+
+AdapterPlan adapter_plan(const mr_adapter_params& p)
+{
+    AdapterPlan w;
+    w.nt = 16;
+    while (w.nt < 256 && w.nt < p.T) w.nt *= 2;
+    w.tiles = (p.T + w.nt - 1) / w.nt;
+    w.rows = rows_for(w.tiles, p.N, 1);
+    w.mt = (p.N + w.rows - 1) / w.rows;
+    w.slices = 1;
+    w.groups = 1;
+    w.bytes = 0;
+    if (p.n_adapters == 0) return w;
+    if (p.rank <= 128) {
+        // as many CTAs as SMs or a little fewer: groups of adapters first (as
+        // many as the tile's tokens can name), then slices of K
+        const int distinct = std::min(std::min(w.nt, p.T), p.n_adapters);
+        const int per_group = std::max(1, 128 / p.rank);
+        w.groups = std::min((distinct + per_group - 1) / per_group, std::max(1, 128 / w.tiles));
+        const int ksteps = (p.K + 63) / 64;
+        w.slices = std::max(1, std::min(std::min(ksteps, 16), 128 / (w.tiles * w.groups)));
+    }
+    w.bytes = static_cast<size_t>(w.slices) * p.T * p.rank * 4;
+    return w;
+}
+
+bool adapter_tensor_path(const mr_adapter_params& p, const AdapterPlan& plan, const void* x, const void* w,
+                         const void* a, const void* b)
+{
+    return p.K % 8 == 0 && aligned(x, 16) && aligned(w, 16) && static_cast<long long>(plan.tiles) * plan.mt < INT_MAX &&
+           (p.n_adapters == 0 || (p.rank % 8 == 0 && p.rank <= 128 && aligned(a, 16) && aligned(b, 16)));
+}
+
 int experts_plain(const mr_expert_params& p, const void* x, const int32_t* idx, const float* w, const void* w13,
                   const void* w2, void* out, unsigned char* ws, const ExpertPlan& plan, int32_t* status,
                   cudaStream_t st)
@@ -420,7 +459,7 @@ int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* 
 size_t moe_adapter_proj_workspace_bytes(const mr_adapter_params* p)
 {
     if (check_adapter(p) != MR_OK || p->T == 0 || p->n_adapters == 0) return 0;
-    return static_cast<size_t>(p->T) * p->rank * 4;
+    return adapter_plan(*p).bytes;
 }
 
 int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* w, const void* a, const void* b,
@@ -440,6 +479,35 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
     using B = __nv_bfloat16;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     float* s = static_cast<float*>(workspace);
+    const AdapterPlan plan = adapter_plan(*p);
+    if (adapter_tensor_path(*p, plan, x, w, a, b)) {
+        CUtensorMap mapw, mapx, mapa;
+        if (!encode_map(&mapw, w, p->K, p->N, 0, plan.rows) || !encode_map(&mapx, x, p->K, p->T, 0, plan.nt))
+            return MR_ECUDA;
+        AdapterArgs d;
+        d.b = static_cast<const B*>(b);
+        d.adapter = adapter;
+        d.scale = scale;
+        d.low = s;
+        d.out = out;
+        d.status = status_word(status);
+        d.range_status = status;
+        d.T = p->T;
+        d.K = p->K;
+        d.N = p->N;
+        d.n_adapters = p->n_adapters;
+        d.rank = p->rank;
+        d.tiles = plan.tiles;
+        d.rows = plan.rows;
+        d.mt = plan.mt;
+        d.slices = plan.slices;
+        wait_test(&d.tries, &d.drop);
+        if (p->n_adapters > 0) {
+            if (!encode_map(&mapa, a, p->K, p->rank, p->n_adapters, p->rank)) return MR_ECUDA;
+            if (launch_adapter_low(plan.nt, mapa, mapx, d, plan.groups, st) != cudaSuccess) return MR_ECUDA;
+        }
+        return from_cuda(launch_adapter_proj(plan.nt, p->out_dtype == MR_F32, mapw, mapx, d, st));
+    }
     const long long T = p->T;
     if (p->n_adapters > 0) {
         const int g = plain_grid(reinterpret_cast<const void*>(&k_adapter_low_plain), T * p->rank);

@@ -43,6 +43,28 @@ int launch_experts_up(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t
 int launch_experts_down(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t, const ExpertArgs& a,
                         long long units, cudaStream_t st);
 
+// What the adapter projection's kernels work on.
+struct AdapterArgs {
+    const __nv_bfloat16* b;    // [n_adapters][N][rank]
+    const int32_t* adapter;    // [T]
+    const float* scale;        // [n_adapters] or null
+    float* low;                // [slices][T][rank] rank-space values, scaled
+    void* out;                 // [T][N]
+    int32_t* status;           // timeouts
+    int32_t* range_status;     // ids past the adapters (nullable)
+    int T, K, N, n_adapters, rank;
+    int tiles;                 // of at most nt tokens
+    int rows, mt;              // weight rows of a stage, row tiles
+    int slices;                // of K, in k_adapter_low
+    int stages, stages_low, drop;
+    uint32_t tries;
+};
+
+int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_x, const AdapterArgs& a, int groups,
+                       cudaStream_t st);
+int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const AdapterArgs& a,
+                        cudaStream_t st);
+
 // A tensor map of bf16 [planes][height][width] (planes 0: a matrix) with boxes
 // of box_h rows by 64 columns, 128-byte swizzled; elements outside read as 0.
 bool encode_map(CUtensorMap* m, const void* base, long long width, long long height, long long planes, int box_h);

@@ -191,8 +191,6 @@ struct GemmBars {
     uint64_t empty[kMaxStages];  // the products have read it
     uint64_t acc_full[2];        // an accumulator is complete
     uint64_t acc_empty[2];       // the epilogue has read it
-    uint64_t low_full[2];        // adapter projection: a chunk of rank-space values is there
-    uint64_t low_empty[2];
     uint64_t drained;            // every product issued is done
     int cols[kMaxStages];        // columns of the unit that starts in this stage
     uint32_t tmem;
