@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
         }
     } else if (warp == 2) {
-        if (lane == 0)
+        if (elect_one())
             for (int g = blockIdx.z; ok && g < groups; g += gridDim.z)
                 for (int k = k0; k < k1; ++k) {
                     ok = pos.wraps == 0 || wait(&bars.empty[pos.s], (pos.wraps - 1) & 1);
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     pos.next(a.stages_low);
                 }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             int seen = 0;
             const uint32_t desc = product_desc(cols);
             for (int g = blockIdx.z; ok && g < groups; g += gridDim.z, ++seen) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_arrive(&bars.acc_empty[buf]);
         }
     }
-    if ((warp == 0 || warp == 2) && lane == 0 && !ok)
+    if ((warp == 0 || warp == 2) && !ok)
         for (int s = 0; s < a.stages_low && s < issued; ++s)
             mbar_wait(&bars.full[s], ((issued - 1 - s) / a.stages_low) & 1, drain);
     __syncwarp();
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     bool ok = true;
 
     if (warp == 0 || warp == 2) {
-        if (lane == 0) {
+        if (elect_one()) {
             for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
                 const int b = u / a.mt, m = u - b * a.mt;
                 for (int k = 0; k < ksteps; ++k) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     mbar_wait(&bars.full[s], ((issued - 1 - s) / a.stages) & 1, drain);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             int seen = 0;
             for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++seen) {
                 const int b = u / a.mt, buf = seen & 1;

@@ -204,7 +204,7 @@ int check_adapter(const mr_adapter_params* p)
 // Workspace of the experts' products: offsets of its parts. The plain kernels
 // use idx, w and h alone.
 struct ExpertPlan {
-    size_t idx, w, h, sids, eids, npp, count, y, sort, sort_bytes, bytes;
+    size_t idx, w, h, xs, sids, eids, npp, count, y, sort, sort_bytes, bytes;
     int nt, cap, rows_up, rows_down, mt_up, mt_down;
 };
 
@@ -261,6 +261,7 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     if (route) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
     w.sort = part(o, w.sort_bytes);
     w.h = part(o, std::max(cap, P) * p.I * 2);
+    w.xs = part(o, w.nt >= kGatherColumns ? cap * p.H * 2 : 0);
     w.y = part(o, P * p.H * 4);
     w.bytes = o;
     return w;
@@ -280,10 +281,16 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
                    cudaStream_t st)
 {
     CUtensorMap map13, mapx, map2, maph;
-    if (!encode_map(&map13, w13, p.H, 2ll * p.I, p.E, plan.rows_up / 2) || !encode_map(&mapx, x, p.H, p.T, 0, 1) ||
-        !encode_map(&map2, w2, p.I, p.H, p.E, plan.rows_down) || !encode_map(&maph, ws + plan.h, p.I, plan.cap, 0, 16))
+    const bool gather = plan.nt >= kGatherColumns;
+    const int box = token_box(plan.nt);
+    if (!encode_map(&map13, w13, p.H, 2ll * p.I, p.E, 16) ||
+        !encode_map(&mapx, gather ? ws + plan.xs : x, p.H, gather ? plan.cap : p.T, 0, gather ? box : 1) ||
+        !encode_map(&map2, w2, p.I, p.H, p.E, plan.rows_down) || !encode_map(&maph, ws + plan.h, p.I, plan.cap, 0, box))
         return MR_ECUDA;
     ExpertArgs a;
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.xs = reinterpret_cast<__nv_bfloat16*>(ws + plan.xs);
+    a.out8 = aligned(out, 8);
     a.sids = reinterpret_cast<int32_t*>(ws + plan.sids);
     a.eids = reinterpret_cast<int32_t*>(ws + plan.eids);
     a.npp = reinterpret_cast<int32_t*>(ws + plan.npp);
@@ -307,7 +314,9 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     const long long blocks = plan.cap / plan.nt;
     a.rows = plan.rows_up;
     a.mt = plan.mt_up;
-    int e = launch_experts_up(plan.nt, map13, mapx, a, blocks * a.mt, st);
+    int e = gather ? launch_experts_gather(a, st) : cudaSuccess;
+    if (e != cudaSuccess) return MR_ECUDA;
+    e = launch_experts_up(plan.nt, map13, mapx, a, blocks * a.mt, st);
     if (e != cudaSuccess) return MR_ECUDA;
     a.rows = plan.rows_down;
     a.mt = plan.mt_down;

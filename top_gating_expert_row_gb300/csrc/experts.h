@@ -8,10 +8,13 @@
 
 namespace mr {
 
-// act(g) in fp32: SiLU g / (1 + exp(-g)), or GELU g * Phi(g).
+// act(g) in fp32: SiLU g / (1 + exp(-g)), or GELU g * Phi(g). The hardware's
+// base-2 exponential and reciprocal are off by a few units of the last place,
+// far below the rounding of h to bf16 that follows.
 __device__ __forceinline__ float act_f32(float g, int act)
 {
-    return act == MR_SILU ? g / (1.0f + expf(-g)) : 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    if (act == MR_SILU) return __fdividef(g, 1.0f + exp2_hw(-g * kLog2e));
+    return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
 }
 
 // Waits on copies in flight when a CTA gives up (attempts of about a microsecond).
@@ -20,6 +23,8 @@ constexpr uint32_t kDrainTries = 1u << 14;
 // What the experts' kernels work on (device pointers; the sorted layout with
 // blocks of nt pairs).
 struct ExpertArgs {
+    const __nv_bfloat16* x;  // [T][H]
+    __nv_bfloat16* xs;     // [cap][H] rows of x in sorted order, where blocks are wide
     const int32_t* sids;   // sorted pair ids, P at sentinels
     const int32_t* eids;   // expert of each block
     const int32_t* npp;    // rows of the sorted layout
@@ -35,9 +40,16 @@ struct ExpertArgs {
     int mt;                // row tiles of this kernel
     int mt_down;           // row tiles of `down`
     int stages, act, drop;
+    int out8;              // out allows 8-byte stores
     uint32_t tries;
 };
 
+// Blocks of this many pairs or more read x from a copy in sorted order.
+constexpr int kGatherColumns = 64;
+// Rows of one copy of the token operand.
+inline int token_box(int nt) { return nt >= 64 ? nt / 4 : 16; }
+
+int launch_experts_gather(const ExpertArgs& a, cudaStream_t st);
 int launch_experts_up(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t, const ExpertArgs& a, long long units,
                       cudaStream_t st);
 int launch_experts_down(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t, const ExpertArgs& a,

@@ -6,7 +6,13 @@
 //
 // Both are one persistent CTA per SM over units (block, row tile); see gemm.cuh
 // for the operands' roles. A unit of `up` holds rows/2 gate rows and the same
-// rows/2 up rows, so that one accumulator has both factors of h.
+// rows/2 up rows, alternating by 16, so that a warp of the epilogue has both
+// factors of h and one shuffle brings them together.
+//
+// Blocks of 64 pairs and more (prompts) read x from a copy in sorted order that
+// k_experts_gather makes: a copy of 4 scattered rows takes the tensor-copy
+// engine 80 clocks, of 64 consecutive rows 120, and each row tile of w13 reads
+// the block's rows again.
 //
 // The sum over a token's slots is taken in slot order by whichever unit
 // completes the token's last slot (a counter per token and row tile): the same
@@ -16,8 +22,14 @@
 
 namespace mr {
 
+namespace {
+constexpr int kTokensAtOnce = 4;  // tokens a warp of the epilogue sums at a time: enough loads in flight
+template <int NT>
+constexpr int kTokenBox = NT >= 64 ? NT / 4 : 16;
+}  // namespace
+
 struct CtaLayout {
-    uint32_t a, b, xchg, info, bars, bytes;
+    uint32_t a, b, info, bars, bytes;
 };
 
 // Offsets from the first 1024-byte boundary of the CTA's shared memory.
@@ -30,8 +42,7 @@ __host__ __device__ inline CtaLayout cta_layout(int nt, int rows, int stages)
     // a product reads 128 rows from the start of a stage, also of the last one
     const uint32_t reach = static_cast<uint32_t>(stages - 1) * rows * kStepBytes + 128 * kStepBytes;
     if (o < reach) o = reach;
-    L.xchg = o; o += 2 * 64 * 17 * 4;
-    L.info = o; o += static_cast<uint32_t>(nt) * 8 + 16;
+    L.info = o; o += static_cast<uint32_t>(nt) * 12 + 16;
     o = (o + 15) / 16 * 16;
     L.bars = o; o += sizeof(GemmBars);
     L.bytes = o + 1024;  // the base is aligned inside
@@ -51,6 +62,44 @@ __device__ __forceinline__ int block_pairs(const int32_t* ids, int P, int lane)
         n += __popc(__ballot_sync(kFull, id >= 0 && id < P));
     }
     return n;
+}
+
+// The counters of `down`, the weighted products of slots without an expert and
+// the output rows of tokens without any; a warp per token.
+__device__ __forceinline__ void prepare_tokens(const ExpertArgs& a, int first, int warps, int lane)
+{
+    for (int t = first; t < a.T; t += warps) {
+        int none = 0;
+        for (int j = 0; j < a.topk; ++j) {
+            const long long pair = static_cast<long long>(t) * a.topk + j;
+            const int e = __ldcg(a.idx + pair);
+            if (e >= 0 && e < a.E) continue;
+            ++none;
+            for (int c = lane * 4; c < a.H; c += 128)
+                *reinterpret_cast<float4*>(a.y + pair * a.H + c) = make_float4(0, 0, 0, 0);
+        }
+        for (int m = lane; m < a.mt_down; m += 32) a.count[static_cast<long long>(t) * a.mt_down + m] = none;
+        if (none == a.topk)
+            for (int c = lane; c < a.H; c += 32) a.out[static_cast<long long>(t) * a.H + c] = __float2bfloat16_rn(0.0f);
+    }
+}
+
+// xs[r] = x[token of sorted row r], and prepare_tokens; a warp per row.
+__global__ void __launch_bounds__(256) k_experts_gather(const __grid_constant__ ExpertArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
+    const int rows = min(__ldcg(a.npp), a.cap);
+    for (int r = warp; r < rows; r += warps) {
+        const int id = __ldcg(a.sids + r);
+        if (id < 0 || id >= a.P) continue;
+        const uint4* src = reinterpret_cast<const uint4*>(a.x + static_cast<long long>(id / a.topk) * a.H);
+        uint4* dst = reinterpret_cast<uint4*>(a.xs + static_cast<long long>(r) * a.H);
+#pragma unroll 4
+        for (int c = lane; c < a.H / 8; c += 32) dst[c] = __ldcg(src + c);
+    }
+    prepare_tokens(a, warp, warps, lane);
 }
 
 template <int NT, bool DOWN>
@@ -103,7 +152,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int issued = 0;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = true;
             for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
                 const int b = u / a.mt, m = u - b * a.mt;
@@ -120,9 +169,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (DOWN) {
                             load_box3(dst, &map_w, k * kStepK, m * a.rows, e, full);
                         } else {
-                            const int half = a.rows >> 1;
-                            load_box3(dst, &map_w, k * kStepK, m * half, e, full);
-                            load_box3(dst + half * kStepBytes, &map_w, k * kStepK, a.I + m * half, e, full);
+                            const int i = m * (a.rows >> 1);
+                            for (int g = 0; g < a.rows >> 5; ++g) {
+                                load_box3(dst + g * 32 * kStepBytes, &map_w, k * kStepK, i + g * 16, e, full);
+                                load_box3(dst + (g * 32 + 16) * kStepBytes, &map_w, k * kStepK, a.I + i + g * 16, e, full);
+                            }
                         }
                     }
                     pos.next(a.stages);
@@ -134,58 +185,53 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
     } else if (warp == 2) {
         if (DOWN) pdl_wait();
+        constexpr bool kScattered = !DOWN && NT < kGatherColumns;
+        const int box = kTokenBox<NT>;
         bool ok = true;
         for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
             const int b = u / a.mt;
             const int32_t* ids = a.sids + static_cast<long long>(b) * NT;
             const int n = block_pairs<NT>(ids, a.P, lane);
-            const int cols = max((n + 15) & ~15, 16);
-            constexpr int kGathers = (NT / 4 + 31) / 32;
-            int4 row[kGathers];
-            if (!DOWN) {
+            const int cols = max((n + 15) & ~15, 16), boxes = (cols + box - 1) / box;
+            int4 row[kScattered ? NT / 4 : 1];
+            if (kScattered) {
 #pragma unroll
-                for (int i = 0; i < kGathers; ++i) {
-                    const int g = i * 32 + lane;
-                    int r[4] = {0, 0, 0, 0};
-                    if (g * 4 < cols)
-                        for (int q = 0; q < 4; ++q) {
-                            const int id = __ldcg(ids + g * 4 + q);
-                            r[q] = id >= 0 && id < a.P ? id / a.topk : 0;  // a sentinel's column is never read
-                        }
-                    row[i] = make_int4(r[0], r[1], r[2], r[3]);
+                for (int g = 0; g < NT / 4; ++g) {
+                    const int4 id = __ldcg(reinterpret_cast<const int4*>(ids + g * 4));
+                    // a sentinel's column is never read
+                    row[g] = make_int4(id.x >= 0 && id.x < a.P ? id.x / a.topk : 0, id.y >= 0 && id.y < a.P ? id.y / a.topk : 0,
+                                       id.z >= 0 && id.z < a.P ? id.z / a.topk : 0, id.w >= 0 && id.w < a.P ? id.w / a.topk : 0);
                 }
             }
-            for (int k = 0; k < ksteps; ++k) {
-                ok = __all_sync(kFull, pos.wraps == 0 || wait(&bars.empty[pos.s], (pos.wraps - 1) & 1));
-                if (!ok) break;
-                uint64_t* full = &bars.full[pos.s];
-                const uint32_t dst = ring_b + pos.s * b_bytes;
-                if (lane == 0) {
+            if (elect_one()) {
+                for (int k = 0; k < ksteps; ++k) {
+                    ok = pos.wraps == 0 || wait(&bars.empty[pos.s], (pos.wraps - 1) & 1);
+                    if (!ok) break;
+                    uint64_t* full = &bars.full[pos.s];
+                    const uint32_t dst = ring_b + pos.s * b_bytes;
                     if (k == 0) bars.cols[pos.s] = cols;
-                    mbar_expect(full, cols * kStepBytes);
-                }
-                ++issued;
-                __syncwarp();
-                if (!a.drop) {
-                    if (DOWN) {
-                        if (lane * 16 < cols)
-                            load_box2(dst + lane * 16 * kStepBytes, &map_t, k * kStepK, b * NT + lane * 16, full);
-                    } else {
+                    mbar_expect(full, (kScattered ? cols : boxes * box) * kStepBytes);
+                    ++issued;
+                    if (!a.drop) {
+                        if (kScattered) {
 #pragma unroll
-                        for (int i = 0; i < kGathers; ++i) {
-                            const int g = i * 32 + lane;
-                            if (g * 4 < cols) load_rows4(dst + g * 4 * kStepBytes, &map_t, k * kStepK, row[i], full);
+                            for (int g = 0; g < NT / 4; ++g)
+                                if (g * 4 < cols) load_rows4(dst + g * 4 * kStepBytes, &map_t, k * kStepK, row[g], full);
+                        } else {
+                            for (int g = 0; g < boxes; ++g)
+                                load_box2(dst + g * box * kStepBytes, &map_t, k * kStepK, b * NT + g * box, full);
                         }
                     }
+                    pos.next(a.stages);
                 }
-                pos.next(a.stages);
+                if (!ok)
+                    for (int s = 0; s < a.stages && s < issued; ++s)
+                        mbar_wait(&bars.full[s], ((issued - 1 - s) / a.stages) & 1, drain);
             }
+            ok = __all_sync(kFull, ok);
         }
-        if (!ok && lane == 0)
-            for (int s = 0; s < a.stages && s < issued; ++s)
-                mbar_wait(&bars.full[s], ((issued - 1 - s) / a.stages) & 1, drain);
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             if (DOWN) pdl_wait();
             int seen = 0;
             bool ok = true;
@@ -217,25 +263,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp >= 4) {
         const int et = threadIdx.x - kEpilogueThreads, q = warp - 4;  // this thread's row of the accumulator
         if (DOWN) pdl_wait();
-        if (!DOWN) {
-            // the counters of `down`, and the rows of tokens without any expert
-            for (int t = blockIdx.x * 4 + q; t < a.T; t += gridDim.x * 4) {
-                int none = 0;
-                for (int j = lane; j < a.topk; j += 32) {
-                    const int e = __ldcg(a.idx + static_cast<long long>(t) * a.topk + j);
-                    none += e < 0 || e >= a.E;
-                }
-                for (int o = 16; o > 0; o >>= 1) none += __shfl_xor_sync(kFull, none, o);
-                for (int m = lane; m < a.mt_down; m += 32) a.count[static_cast<long long>(t) * a.mt_down + m] = none;
-                if (none == a.topk)
-                    for (int c = lane; c < a.H; c += 32)
-                        a.out[static_cast<long long>(t) * a.H + c] = __float2bfloat16_rn(0.0f);
-            }
-        }
-        float* xchg = reinterpret_cast<float*>(smem + L.xchg);
-        int* info = reinterpret_cast<int*>(smem + L.info);  // NT pair ids, then NT weights
+        if (!DOWN && NT < kGatherColumns) prepare_tokens(a, blockIdx.x * 4 + q, gridDim.x * 4, lane);
+        int* info = reinterpret_cast<int*>(smem + L.info);  // NT pair ids, NT weights, NT completed tokens and their number
         float* info_w = reinterpret_cast<float*>(info + NT);
-        int* ndone = info + 2 * NT;
+        int* done = info + 2 * NT;
+        int* ndone = info + 3 * NT;
         int seen = 0;
         for (int u = blockIdx.x; u < units; u += gridDim.x, ++seen) {
             const int b = u / a.mt, m = u - b * a.mt, buf = seen & 1;
@@ -265,52 +297,66 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 tc_fence_before();
                 mbar_arrive(&bars.acc_empty[buf]);
+                // this unit's products before its counts, everyone's counts before their products
                 __threadfence();
                 epilogue_sync();
                 for (int c = et; c < n; c += kEpilogueThreads) {
                     const int t = info[c] / a.topk;
-                    const int old = atomicAdd(a.count + static_cast<long long>(t) * a.mt_down + m, 1);
-                    if (old == a.topk - 1) reinterpret_cast<int*>(xchg)[atomicAdd(ndone, 1)] = t;
+                    if (atomicAdd(a.count + static_cast<long long>(t) * a.mt_down + m, 1) == a.topk - 1)
+                        done[atomicAdd(ndone, 1)] = t;
                 }
-                epilogue_sync();
                 __threadfence();
-                const int done = *ndone;
-                for (int i = 0; i < done; ++i) {
-                    const long long t = reinterpret_cast<int*>(xchg)[i];
-                    if (!mine) continue;
-                    float sum = 0.0f;
-                    for (int j = 0; j < a.topk; ++j) {
-                        const int e = __ldcg(a.idx + t * a.topk + j);
-                        const float y = __ldcg(a.y + (t * a.topk + j) * a.H + row);
-                        if (e >= 0 && e < a.E) sum += y;
+                epilogue_sync();
+                // four rows a lane; tokens side by side where the tile has fewer than 128 rows
+                const int lanes = a.rows >> 2, per_warp = 32 / lanes, r = m * a.rows + (lane % lanes) * 4;
+                const int nd = *ndone;
+                if (r < a.H)
+                    for (int i = q * per_warp + lane / lanes; i < nd; i += 4 * per_warp * kTokensAtOnce) {
+                        float4 sum[kTokensAtOnce];
+                        const float* y[kTokensAtOnce];
+#pragma unroll
+                        for (int k = 0; k < kTokensAtOnce; ++k) {
+                            const int at = min(i + k * 4 * per_warp, nd - 1);
+                            y[k] = a.y + static_cast<long long>(done[at]) * a.topk * a.H + r;
+                            sum[k] = make_float4(0, 0, 0, 0);
+                        }
+#pragma unroll 2
+                        for (int j = 0; j < a.topk; ++j)
+#pragma unroll
+                            for (int k = 0; k < kTokensAtOnce; ++k) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(y[k] + static_cast<long long>(j) * a.H));
+                                sum[k].x += v.x; sum[k].y += v.y; sum[k].z += v.z; sum[k].w += v.w;
+                            }
+#pragma unroll
+                        for (int k = 0; k < kTokensAtOnce; ++k)
+                            if (i + k * 4 * per_warp < nd) {
+                                const float v[4] = {sum[k].x, sum[k].y, sum[k].z, sum[k].w};
+                                __nv_bfloat16* o = a.out + static_cast<long long>(done[i + k * 4 * per_warp]) * a.H + r;
+                                if (a.out8) store4(o, v);
+                                else
+                                    for (int z = 0; z < 4; ++z) o[z] = __float2bfloat16_rn(v[z]);
+                            }
                     }
-                    a.out[t * a.H + row] = __float2bfloat16_rn(sum);
-                }
                 epilogue_sync();  // the next unit overwrites info
             } else {
-                const int half = a.rows >> 1;
-                const bool gate = et < half, up = et >= half && et < a.rows;
-                const int i = gate ? et : et - half, col = m * half + i;
-                const bool mine = (gate || up) && col < a.I;
-                float* to_up = xchg + i * 17;              // gate rows' later columns
-                float* to_gate = xchg + (64 + i) * 17;     // up rows' earlier columns
-                for (int c0 = 0; c0 < n; c0 += 16) {
-                    float v[16];
-                    tmem_load16(acc + c0, v);
-                    if (gate)
-                        for (int c = 8; c < 16; ++c) to_up[c] = v[c];
-                    else if (up)
-                        for (int c = 0; c < 8; ++c) to_gate[c] = v[c];
-                    epilogue_sync();
+                // lanes 0-15 hold gate rows, lanes 16-31 the same up rows: the
+                // first finish the even columns, the others the odd ones
+                const bool low = lane < 16;
+                const int col = m * (a.rows >> 1) + q * 16 + (lane & 15);
+                const bool mine = q * 32 < a.rows && col < a.I;
+                __nv_bfloat16* h = a.h + (static_cast<long long>(b) * NT + (low ? 0 : 1)) * a.I + col;
+                if (q * 32 < a.rows)
+                    for (int c0 = 0; c0 < n; c0 += 16) {
+                        float v[16];
+                        tmem_load16(acc + c0, v);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int at = c0 + (gate ? c : c + 8);
-                        const float g = gate ? v[c] : to_up[c + 8], w = gate ? to_gate[c] : v[c + 8];
-                        if (mine && at < n)
-                            a.h[(static_cast<long long>(b) * NT + at) * a.I + col] = __float2bfloat16_rn(act_f32(g, a.act) * w);
+                        for (int c = 0; c < 16; c += 2) {
+                            const float other = __shfl_xor_sync(kFull, low ? v[c + 1] : v[c], 16);
+                            const float g = low ? v[c] : other, w = low ? other : v[c + 1];
+                            if (mine && c0 + c + (low ? 0 : 1) < n)
+                                h[static_cast<long long>(c0 + c) * a.I] = __float2bfloat16_rn(act_f32(g, a.act) * w);
+                        }
                     }
-                    epilogue_sync();
-                }
                 tc_fence_before();
                 mbar_arrive(&bars.acc_empty[buf]);
             }
@@ -324,6 +370,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tmem_free(tmem, kColumns);
     }
     if (threadIdx.x == 0 && bars.gone) report_status(a.status, kStatusTimeout);
+}
+
+int launch_experts_gather(const ExpertArgs& a, cudaStream_t st)
+{
+    const int grid = persistent_grid(reinterpret_cast<const void*>(&k_experts_gather), 256, 0, (a.cap + 7) / 8);
+    if (grid < 1) return cudaErrorLaunchOutOfResources;
+    return launch_kernel(&k_experts_gather, dim3(grid), dim3(256), 0, st, 0, a);
 }
 
 namespace {
