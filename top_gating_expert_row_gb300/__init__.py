@@ -13,6 +13,7 @@ tensors and call the entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -98,7 +99,9 @@ class _Lib:
     def __getattr__(self, name):
         if _Lib._cdll is None:
             _Lib._cdll = _load()
-        return getattr(_Lib._cdll, name)
+        fn = getattr(_Lib._cdll, name)
+        setattr(self, name, fn)  # found at once from now on
+        return fn
 
 
 def _load():
@@ -507,35 +510,51 @@ def aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor, T: in
 
 
 def _check(what: str, t: torch.Tensor, shape, dtype, device) -> None:
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, x on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _check_status(status, device) -> Optional[int]:
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise ValueError("status must hold an int32")
+    _check("status", status, status.shape, torch.int32, device)
+    return status.data_ptr()
 
 
 class _Launch:
     """The device of x made current, and on it `stream` (default: that device's current stream), on which the
-    call's tensors are allocated, so that a workspace is not reused before the call's kernels are done."""
+    call's tensors are allocated, so that a workspace is not reused before the call's kernels are done. Entering
+    gives the stream's handle."""
 
-    __slots__ = ("device", "stream")
+    __slots__ = ("index", "device", "stream")
 
     def __init__(self, device, stream):
         if device.type != "cuda":
             raise ValueError(f"x must be on a CUDA device, got {device}")
-        self.device = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, x on {device}")
-        self.stream = None if stream is None else torch.cuda.stream(stream)
+        self.index, self.device, self.stream = device.index, None, None
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, x on {device}")
+            self.stream = torch.cuda.stream(stream)
+        elif self.index != torch.cuda.current_device():
+            self.device = torch.cuda.device(device)
 
     def __enter__(self):
         if self.device is not None:
             self.device.__enter__()
         if self.stream is not None:
             self.stream.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.stream is not None:
@@ -544,14 +563,36 @@ class _Launch:
             self.device.__exit__(*exc)
 
 
+# The options of a call and the workspace it needs depend on its sizes alone: kept, so that a decode step does not
+# build them again (and nothing else is).
+
+
+@functools.lru_cache(maxsize=1024)
+def _experts_plan(T, H, I, E, topk, act):
+    p = mr_expert_params(T, H, I, E, topk, MR_BF16, act)
+    return ctypes.byref(p), moe_experts_workspace_bytes(p)
+
+
+@functools.lru_cache(maxsize=1024)
+def _layer_plan(H, I, act, *options):
+    cp = mr_router_params(*options, None)
+    return ctypes.byref(cp), moe_layer_workspace_bytes(cp, H, I, act)
+
+
+@functools.lru_cache(maxsize=1024)
+def _adapter_plan(T, K, N, n, rank, out_f32):
+    p = mr_adapter_params(T, K, N, n, rank, MR_BF16, MR_F32 if out_f32 else MR_BF16)
+    return ctypes.byref(p), moe_adapter_proj_workspace_bytes(p)
+
+
 def _weights_shape(x, w13, w2):
     if x.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
         raise ValueError("x is [T, H], w13 [E, 2*I, H], w2 [E, H, I]")
-    E, I = w13.shape[0], w2.shape[2]
-    H = x.shape[1]
-    _check("x", x, x.shape, torch.bfloat16, x.device)
-    _check("w13", w13, (E, 2 * I, H), torch.bfloat16, x.device)
-    _check("w2", w2, (E, H, I), torch.bfloat16, x.device)
+    E, H, I = w2.shape
+    device = x.device
+    _check("x", x, (x.shape[0], H), torch.bfloat16, device)
+    _check("w13", w13, (E, 2 * I, H), torch.bfloat16, device)
+    _check("w2", w2, (E, H, I), torch.bfloat16, device)
     return E, H, I
 
 
@@ -561,32 +602,48 @@ def experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, w13: 
     the experts topk_idx [T, topk] (int32; ids outside [0, E) are skipped) with weights topk_w (fp32).
     w13 [E, 2*I, H] holds each expert's gate rows, then its up rows; w2 is [E, H, I]."""
     E, H, I = _weights_shape(x, w13, w2)
-    T, k = topk_idx.shape if topk_idx.dim() == 2 else (-1, -1)
-    _check("topk_idx", topk_idx, (x.shape[0], k), torch.int32, x.device)
-    _check("topk_w", topk_w, (T, k), torch.float32, x.device)
-    p = mr_expert_params(T, H, I, E, k, MR_BF16, act)
-    with _Launch(x.device, stream):
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx is [T, topk]")
+    T, k, dev = x.shape[0], topk_idx.shape[1], x.device
+    _check("topk_idx", topk_idx, (T, k), torch.int32, dev)
+    _check("topk_w", topk_w, (T, k), torch.float32, dev)
+    st = _check_status(status, dev)
+    p, nb = _experts_plan(T, H, I, E, k, act)
+    with _Launch(dev, stream) as raw:
         out = torch.empty_like(x)
-        ws = torch.empty(max(1, moe_experts_workspace_bytes(p)), dtype=torch.uint8, device=x.device)
-        moe_experts_fwd(p, x, topk_idx, topk_w, w13, w2, out, ws, None, status)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        _ok(_lib.moe_experts_fwd(p, x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), w13.data_ptr(),
+                                 w2.data_ptr(), out.data_ptr(), ws.data_ptr(), nb, st, raw), "moe_experts_fwd")
     return out
 
 
 def layer(x: torch.Tensor, logits: torch.Tensor, topk: int, w13: torch.Tensor, w2: torch.Tensor, act: int = MR_SILU,
-          status: Optional[torch.Tensor] = None, stream=None, **kw) -> dict:
+          status: Optional[torch.Tensor] = None, stream=None, score_fn: int = MR_SOFTMAX, renorm: int = 0,
+          n_group: int = 0, topk_group: int = 0, n_shared: int = 0, scaling: float = 1.0, shared_weight: float = 1.0,
+          bias: Optional[torch.Tensor] = None) -> dict:
     """moe_layer_fwd with freshly allocated outputs: the layer's out [T, H] and the routing it took (topk_idx,
-    topk_w) from x [T, H] (bf16) and router logits [T, E] (fp32 or bf16). Routing options (score_fn, renorm,
-    n_shared, ...) as for route(); w13 / w2 as for experts(), with the shared experts last."""
+    topk_w) from x [T, H] (bf16) and router logits [T, E] (fp32 or bf16). Routing options as for route(); w13 / w2
+    as for experts(), with the shared experts last."""
     E_tot, H, I = _weights_shape(x, w13, w2)
-    p = params_for(logits, topk, **kw)
-    _check("logits", logits, (x.shape[0], E_tot - p.n_shared), logits.dtype, x.device)
-    cp = p.c()
-    with _Launch(x.device, stream):
+    T, E, dev = x.shape[0], E_tot - n_shared, x.device
+    dtype = _dtype_code(logits)
+    _check("logits", logits, (T, E), logits.dtype, dev)
+    st = _check_status(status, dev)
+    options = (T, E, topk, score_fn, dtype, int(renorm), n_group, topk_group, n_shared, scaling, shared_weight)
+    if bias is None:
+        p, nb = _layer_plan(H, I, act, *options)
+    else:
+        _check("bias", bias, (E,), torch.float32, dev)
+        cp = mr_router_params(*options, bias.data_ptr())
+        p, nb = ctypes.byref(cp), moe_layer_workspace_bytes(cp, H, I, act)
+    with _Launch(dev, stream) as raw:
         out = torch.empty_like(x)
-        idx = torch.empty(p.T, topk, dtype=torch.int32, device=x.device)
-        w = torch.empty(p.T, topk, dtype=torch.float32, device=x.device)
-        ws = torch.empty(max(1, moe_layer_workspace_bytes(cp, H, I, act)), dtype=torch.uint8, device=x.device)
-        moe_layer_fwd(cp, H, I, act, x, logits, w13, w2, out, idx, w, ws, None, status)
+        idx = torch.empty(T, max(topk, 0), dtype=torch.int32, device=dev)
+        w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        _ok(_lib.moe_layer_fwd(p, H, I, act, x.data_ptr(), logits.data_ptr(), w13.data_ptr(), w2.data_ptr(),
+                               out.data_ptr(), idx.data_ptr(), w.data_ptr(), ws.data_ptr(), nb, st, raw),
+            "moe_layer_fwd")
     return dict(out=out, topk_idx=idx, topk_w=w)
 
 
@@ -604,20 +661,26 @@ def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = N
     _check("w", w, (N, K), torch.bfloat16, dev)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    st = _check_status(status, dev)
     n = rank = 0
-    if a is not None or b is not None or adapter is not None:
+    pa = pb = pi = ps = None
+    if a is not None or b is not None or adapter is not None or scale is not None:
         if a is None or b is None or adapter is None:
             raise ValueError("a, b and adapter come together")
-        n, rank = a.shape[:2] if a.dim() == 3 else (-1, -1)
+        if a.dim() != 3:
+            raise ValueError("a is [n, rank, K], b [n, N, rank]")
+        n, rank = a.shape[:2]
         _check("a", a, (n, rank, K), torch.bfloat16, dev)
         _check("b", b, (n, N, rank), torch.bfloat16, dev)
         _check("adapter", adapter, (T,), torch.int32, dev)
+        pa, pb, pi = a.data_ptr(), b.data_ptr(), adapter.data_ptr()
         if scale is not None:
             _check("scale", scale, (n,), torch.float32, dev)
-    p = mr_adapter_params(T, K, N, n, rank, MR_BF16, MR_F32 if out_dtype == torch.float32 else MR_BF16)
-    with _Launch(dev, stream):
+            ps = scale.data_ptr()
+    p, nb = _adapter_plan(T, K, N, n, rank, out_dtype == torch.float32)
+    with _Launch(dev, stream) as raw:
         out = torch.empty(T, N, dtype=out_dtype, device=dev)
-        nb = moe_adapter_proj_workspace_bytes(p)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-        moe_adapter_proj_fwd(p, x, w, a, b, adapter, scale, out, ws, nb, status)
+        _ok(_lib.moe_adapter_proj_fwd(p, x.data_ptr(), w.data_ptr(), pa, pb, pi, ps, out.data_ptr(),
+                                      ws.data_ptr() if nb else None, nb, st, raw), "moe_adapter_proj_fwd")
     return out

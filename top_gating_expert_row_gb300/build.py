@@ -1,7 +1,7 @@
 """Build libmoerouter.so for sm_103a with nvcc, in-tree.
 
-Translation units compile in parallel (fwd.cu once per score function x logits
-dtype, plus sort.cu, bwd.cu, aux_loss.cu, experts.cu, experts_mma.cu,
+Translation units compile in parallel (fwd.cu and layer_few.cu once per score
+function x logits dtype, plus sort.cu, bwd.cu, aux_loss.cu, experts.cu, experts_mma.cu,
 adapter_mma.cu, api.cu) and link into one shared library with the
 static CUDA runtime, so loading it needs no CUDA library path.
 
@@ -34,6 +34,10 @@ UNITS = [
     ("sort", "sort.cu", []),
     ("bwd", "bwd.cu", []),
     ("aux_loss", "aux_loss.cu", []),
+    ("layer_few_s0_d0", "layer_few.cu", ["-DMR_SCORE_FN=0", "-DMR_IN_BF16=0"]),
+    ("layer_few_s0_d1", "layer_few.cu", ["-DMR_SCORE_FN=0", "-DMR_IN_BF16=1"]),
+    ("layer_few_s1_d0", "layer_few.cu", ["-DMR_SCORE_FN=1", "-DMR_IN_BF16=0"]),
+    ("layer_few_s1_d1", "layer_few.cu", ["-DMR_SCORE_FN=1", "-DMR_IN_BF16=1"]),
     ("experts", "experts.cu", []),
     ("experts_mma", "experts_mma.cu", []),
     ("adapter_mma", "adapter_mma.cu", []),

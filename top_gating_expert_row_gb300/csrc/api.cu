@@ -462,6 +462,13 @@ int check_sort(int T, int topk, int E_tot, int block_m)
 
 int router_check(const mr_router_params* p) { return check_router(p); }
 
+RouteArgs router_args(const mr_router_params* p, const void* logits)
+{
+    return route_args(p, logits, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+}
+
+bool router_forced_select() { return g_path.forced() == 2; }
+
 int32_t* status_word(int32_t* status) { return status ? status : device_status_address(); }
 
 void wait_test(uint32_t* tries, int* drop)

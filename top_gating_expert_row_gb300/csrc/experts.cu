@@ -6,7 +6,7 @@
 
 #include <algorithm>
 
-#include "experts.h"
+#include "few.cuh"
 
 namespace mr {
 
@@ -151,6 +151,28 @@ __global__ void k_adapter_proj_plain(const __nv_bfloat16* x, const __nv_bfloat16
     }
 }
 
+// ---- a few pairs ---------------------------------------------------------------------------------------------------
+
+// few.cuh's kernels for a given choice of experts.
+template <bool DOWN>
+__global__ void __launch_bounds__(kFewThreads, 2) k_experts_few(FewArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    few_body<DOWN>(a, smem, [&](int32_t* s_idx, float* s_w) {
+        for (int p = threadIdx.x; p < a.T * a.topk; p += kFewThreads) {
+            const int e = __ldcg(a.idx + p);
+            s_idx[p] = e;
+            s_w[p] = __ldcg(a.w + p);
+            if (!DOWN && blockIdx.x == 0 && (e < 0 || e >= a.E)) report_status(a.status, kStatusRange);
+        }
+    });
+}
+
+int launch_layer_few_s0_d0(const RouteArgs&, const FewArgs&, int, bool, cudaStream_t);
+int launch_layer_few_s0_d1(const RouteArgs&, const FewArgs&, int, bool, cudaStream_t);
+int launch_layer_few_s1_d0(const RouteArgs&, const FewArgs&, int, bool, cudaStream_t);
+int launch_layer_few_s1_d1(const RouteArgs&, const FewArgs&, int, bool, cudaStream_t);
+
 namespace {
 
 constexpr int kPlainThreads = 256;
@@ -265,6 +287,62 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     w.y = part(o, P * p.H * 4);
     w.bytes = o;
     return w;
+}
+
+// Few pairs: each pair's weights are read by itself, so the tensor cores' path
+// (which reads an expert's weights once for all its pairs) is left only while
+// there are about as many experts in use as pairs.
+constexpr int kFewPairs = 32, kFewTokens = 8;
+constexpr size_t kFewSmem = 64 * 1024;
+
+bool few_path(const mr_expert_params& p, const void* x, const void* w13, const void* w2)
+{
+    const long long P = static_cast<long long>(p.T) * p.topk;
+    return P <= kFewPairs && p.T <= kFewTokens && p.H % 8 == 0 && p.I % 8 == 0 && aligned(x, 16) && aligned(w13, 16) &&
+           aligned(w2, 16) && static_cast<size_t>(P) * p.I * 2 <= kFewSmem && static_cast<size_t>(p.T) * p.H * 2 <= kFewSmem;
+}
+
+FewArgs few_args(const mr_expert_params& p, const void* x, const void* w13, const void* w2, void* out, void* h)
+{
+    FewArgs a;
+    a.x = static_cast<const __nv_bfloat16*>(x);
+    a.w13 = static_cast<const __nv_bfloat16*>(w13);
+    a.w2 = static_cast<const __nv_bfloat16*>(w2);
+    a.h = static_cast<__nv_bfloat16*>(h);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.idx = nullptr;
+    a.w = nullptr;
+    a.idx_out = nullptr;
+    a.w_out = nullptr;
+    a.status = nullptr;
+    a.T = p.T;
+    a.topk = p.topk;
+    a.H = p.H;
+    a.I = p.I;
+    a.E = p.E;
+    a.act = p.act;
+    return a;
+}
+
+template <bool DOWN>
+int launch_experts_few(const FewArgs& a, cudaStream_t st)
+{
+    const void* f = reinterpret_cast<const void*>(&k_experts_few<DOWN>);
+    const size_t smem = few_smem(a, DOWN, 0);
+    const int e = ensure_smem(f, smem);
+    if (e != cudaSuccess) return e;
+    const long long tasks = static_cast<long long>(a.T) * (DOWN ? a.H : a.topk * a.I);
+    const int grid = persistent_grid(f, kFewThreads, smem, (tasks + kFewWarps - 1) / kFewWarps);
+    if (grid < 1) return cudaErrorLaunchOutOfResources;
+    return launch_kernel(&k_experts_few<DOWN>, dim3(grid), dim3(kFewThreads), smem, st, 0, a);
+}
+
+int launch_layer_few(const mr_router_params* p, const RouteArgs& r, const FewArgs& a, bool down, cudaStream_t st)
+{
+    const int nv = nv_index(p->E);
+    if (p->score_fn == MR_SOFTMAX)
+        return p->in_dtype == MR_BF16 ? launch_layer_few_s0_d1(r, a, nv, down, st) : launch_layer_few_s0_d0(r, a, nv, down, st);
+    return p->in_dtype == MR_BF16 ? launch_layer_few_s1_d1(r, a, nv, down, st) : launch_layer_few_s1_d0(r, a, nv, down, st);
 }
 
 // Whether the tensor-core kernels' copies can address these arrays: 16-byte
@@ -408,6 +486,14 @@ int moe_experts_fwd(const mr_expert_params* p, const void* x, const int32_t* top
     if (ws_bytes < plan.bytes || !aligned(workspace, 256)) return MR_EINVAL;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
+    if (few_path(*p, x, w13, w2)) {
+        FewArgs a = few_args(*p, x, w13, w2, out, ws + plan.h);
+        a.idx = topk_idx;
+        a.w = topk_w;
+        a.status = status;
+        const int e = launch_experts_few<false>(a, st);
+        return e != cudaSuccess ? MR_ECUDA : from_cuda(launch_experts_few<true>(a, st));
+    }
     if (!tensor_path(*p, plan, x, w13, w2))
         return experts_plain(*p, x, topk_idx, topk_w, w13, w2, out, ws, plan, status, st);
     const int e = moe_sort(topk_idx, nullptr, p->T, p->topk, p->E, plan.nt, reinterpret_cast<int32_t*>(ws + plan.sids),
@@ -446,6 +532,14 @@ int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* 
     int32_t* idx = topk_idx ? topk_idx : reinterpret_cast<int32_t*>(ws + plan.idx);
     float* w = topk_w ? topk_w : reinterpret_cast<float*>(ws + plan.w);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (few_path(q, x, w13, w2) && p->E <= 128 * kRegisterMaxNv && !router_forced_select()) {
+        FewArgs a = few_args(q, x, w13, w2, out, ws + plan.h);
+        a.idx_out = topk_idx;
+        a.w_out = topk_w;
+        const RouteArgs r = router_args(p, logits);
+        const int e = launch_layer_few(p, r, a, false, st);
+        return e != cudaSuccess ? MR_ECUDA : from_cuda(launch_layer_few(p, r, a, true, st));
+    }
     if (!tensor_path(q, plan, x, w13, w2)) {
         rc = moe_router_fwd(p, logits, nullptr, nullptr, nullptr, idx, w, status, stream);
         return rc != MR_OK ? rc : experts_plain(q, x, idx, w, w13, w2, out, ws, plan, status, st);

@@ -84,6 +84,8 @@ bool encode_map(CUtensorMap* m, const void* base, long long width, long long hei
 // The validation of the forward calls' options, the per-device status word and
 // the wait-test settings (api.cu).
 int router_check(const mr_router_params* p);
+RouteArgs router_args(const mr_router_params* p, const void* logits);
+bool router_forced_select();
 int32_t* status_word(int32_t* status);
 void wait_test(uint32_t* tries, int* drop);
 
