@@ -14,7 +14,7 @@
 //
 // k_adapter_proj starts while k_adapter_low runs (its sum over K needs nothing
 // of it), so the low-rank product costs little time of its own once w is large.
-#include "experts.h"
+#include "few.cuh"
 #include "gemm.cuh"
 
 namespace mr {
@@ -235,6 +235,113 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (threadIdx.x == 0 && bars.gone) report_status(a.status, kStatusTimeout);
 }
 
+// The same without tiles, for calls whose products are few: a warp takes four
+// ranks of one token, and a's rows come from L2 again for each token.
+__global__ void __launch_bounds__(256) k_adapter_low_rows(const __nv_bfloat16* x, const __nv_bfloat16* wa, AdapterArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    constexpr int kAtOnce = 4;
+    const int lane = threadIdx.x & 31, K8 = a.K / 8, quads = (a.rank + 3) / 4;
+    const long long warps = static_cast<long long>(gridDim.x) * 8;
+    for (long long u = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < static_cast<long long>(a.T) * quads;
+         u += warps) {
+        const long long t = u / quads;
+        const int r0 = static_cast<int>(u - t * quads) * 4;
+        const int id = __ldcg(a.adapter + t);
+        if (id >= a.n_adapters && r0 == 0 && lane == 0) report_status(a.range_status, kStatusRange);
+        if (id < 0 || id >= a.n_adapters) continue;
+        const uint4* xr = reinterpret_cast<const uint4*>(x + t * a.K);
+        const uint4* ar = reinterpret_cast<const uint4*>(wa + (static_cast<long long>(id) * a.rank + r0) * a.K);
+        float sum[4] = {0, 0, 0, 0};  // rank is a multiple of 8: all four rows are there
+        for (int c0 = lane; c0 < K8; c0 += 32 * kAtOnce) {
+            uint4 xc[kAtOnce], ac[kAtOnce][4];
+#pragma unroll
+            for (int c = 0; c < kAtOnce; ++c)
+                if (c0 + c * 32 < K8) {
+                    xc[c] = __ldcg(xr + c0 + c * 32);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) ac[c][q] = __ldcg(ar + static_cast<long long>(q) * K8 + c0 + c * 32);
+                }
+#pragma unroll
+            for (int c = 0; c < kAtOnce; ++c)
+                if (c0 + c * 32 < K8) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) sum[q] = dot8(ac[c][q], xc[c], sum[q]);
+                }
+        }
+        const float sc = a.scale ? __ldcg(a.scale + id) : 1.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float v = warp_sum(sum[q]);
+            if (lane == q) a.low[t * a.rank + r0 + q] = v * sc;
+        }
+    }
+}
+
+// One to TOKENS tokens: a warp per row of w, on the CUDA cores (few.cuh says
+// why). The row's product, and the loads of b's row, come before the wait for
+// the rank-space values; the lanes share out the ranks.
+template <int TOKENS, typename OutT>
+__global__ void __launch_bounds__(256) k_adapter_few(const __nv_bfloat16* x, const __nv_bfloat16* w, AdapterArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    const bool low = a.n_adapters > 0;
+    if (!low) pdl_wait();
+    const int lane = threadIdx.x & 31, K8 = a.K / 8;
+    for (int i = threadIdx.x; i < a.T * K8; i += 256)
+        reinterpret_cast<uint4*>(smem)[i] = __ldcg(reinterpret_cast<const uint4*>(x) + i);
+    __syncthreads();
+    const uint4* xs = reinterpret_cast<const uint4*>(smem);
+    constexpr int kChunks = 8;
+    bool waited = !low;
+    for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < a.N; row += gridDim.x * 8) {
+        const uint4* wr = reinterpret_cast<const uint4*>(w + static_cast<long long>(row) * a.K);
+        float sum[TOKENS] = {};
+        for (int c0 = lane; c0 < K8; c0 += 32 * kChunks) {
+            uint4 wc[kChunks];
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+                if (c0 + c * 32 < K8) wc[c] = load_weights(wr + c0 + c * 32);
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+                if (c0 + c * 32 < K8) {
+#pragma unroll
+                    for (int t = 0; t < TOKENS; ++t)
+                        if (t < a.T) sum[t] = dot8(wc[c], xs[t * K8 + c0 + c * 32], sum[t]);
+                }
+        }
+        if (low) {
+            int id[TOKENS];
+            float b0[TOKENS];
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) {
+                id[t] = t < a.T ? __ldcg(a.adapter + t) : -1;
+                if (id[t] >= a.n_adapters) id[t] = -1;
+                b0[t] = 0.0f;
+                if (id[t] >= 0 && lane < a.rank)
+                    b0[t] = load_scalar(a.b + (static_cast<long long>(id[t]) * a.N + row) * a.rank + lane);
+            }
+            if (!waited) pdl_wait();
+            waited = true;
+#pragma unroll
+            for (int t = 0; t < TOKENS; ++t) {
+                if (id[t] < 0) continue;
+                const __nv_bfloat16* br = a.b + (static_cast<long long>(id[t]) * a.N + row) * a.rank;
+                const float* s = a.low + static_cast<long long>(t) * a.rank;
+                if (lane < a.rank) sum[t] = fmaf(b0[t], __ldcg(s + lane), sum[t]);
+                for (int r = lane + 32; r < a.rank; r += 32) sum[t] = fmaf(load_scalar(br + r), __ldcg(s + r), sum[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t) {
+            const float v = warp_sum(sum[t]);
+            if (lane == 0 && t < a.T) store_scalar(static_cast<OutT*>(a.out) + static_cast<long long>(t) * a.N + row, v);
+        }
+    }
+    if (!waited) pdl_wait();  // a kernel never ends before the one it follows
+}
+
 // ---- projection --------------------------------------------------------------------------------------------------
 
 // Sum over the slices of four rank-space values.
@@ -258,20 +365,6 @@ __device__ __forceinline__ void unpack8(uint4 p, float (&v)[8])
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-}
-
-// b[row] . s over the ranks; b in device memory, s fp32 with `step` floats from rank to rank.
-__device__ __forceinline__ float rank_dot(const __nv_bfloat16* brow, const float* s, int step, int rank)
-{
-    float v = 0.0f;
-#pragma unroll 2
-    for (int r = 0; r < rank; r += 8) {
-        float w[8];
-        unpack8(__ldcg(reinterpret_cast<const uint4*>(brow + r)), w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v = fmaf(w[i], s[(r + i) * step], v);
-    }
-    return v;
 }
 
 template <int NT, typename OutT>
@@ -396,11 +489,39 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                     epilogue_sync();
                     const int er = et % a.rows, orow = m * a.rows + er;
-                    for (int t = et / a.rows; t < tokens; t += kEpilogueThreads / a.rows)
-                        part[t * a.rows + er] =
-                            mine[t] >= 0 && orow < a.N
-                                ? rank_dot(a.b + (static_cast<long long>(mine[t]) * a.N + orow) * rank, s + t * rank, 1, rank)
-                                : 0.0f;
+                    // this thread's row of the unit, every (128 / rows)-th token, 4 of them at a time
+                    const int every = kEpilogueThreads / a.rows;
+                    for (int tb = et / a.rows; tb < tokens; tb += 4 * every) {
+                        float v[4] = {0, 0, 0, 0};
+                        const __nv_bfloat16* brow[4];
+                        bool use[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int t = tb + k * every;
+                            use[k] = t < tokens && mine[t] >= 0 && orow < a.N;
+                            brow[k] = a.b + (use[k] ? (static_cast<long long>(mine[t]) * a.N + orow) * rank : 0);
+                        }
+#pragma unroll 2
+                        for (int r = 0; r < rank; r += 8) {
+                            uint4 p[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (use[k]) p[k] = __ldcg(reinterpret_cast<const uint4*>(brow[k] + r));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (!use[k]) continue;
+                                float w[8];
+                                unpack8(p[k], w);
+                                const float4* x = reinterpret_cast<const float4*>(s + (tb + k * every) * rank + r);
+                                const float4 y = x[0], z = x[1];
+                                v[k] = fmaf(w[0], y.x, fmaf(w[1], y.y, fmaf(w[2], y.z, fmaf(w[3], y.w, v[k]))));
+                                v[k] = fmaf(w[4], z.x, fmaf(w[5], z.y, fmaf(w[6], z.z, fmaf(w[7], z.w, v[k]))));
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (tb + k * every < tokens) part[(tb + k * every) * a.rows + er] = v[k];
+                    }
                 }
                 tile = b;
             }
@@ -466,11 +587,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 }
                             }
                         } else if (there) {
+                            // each token with its own row of b, 16 loads in flight
+                            for (int r = 0; r < rank; r += 8) {
+                                uint4 p[16];
 #pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                if (mine[c0 + c] >= 0)
-                                    v[c] += rank_dot(a.b + (static_cast<long long>(mine[c0 + c]) * a.N + row) * rank, s + c,
-                                                     16, rank);
+                                for (int c = 0; c < 16; ++c)
+                                    if (mine[c0 + c] >= 0)
+                                        p[c] = __ldcg(reinterpret_cast<const uint4*>(
+                                            a.b + (static_cast<long long>(mine[c0 + c]) * a.N + row) * rank + r));
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    if (mine[c0 + c] < 0) continue;
+                                    float w[8];
+                                    unpack8(p[c], w);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) v[c] = fmaf(w[i], s[(r + i) * 16 + c], v[c]);
+                                }
+                            }
                         }
                     }
                 }
@@ -530,6 +663,32 @@ int launch_proj(const CUtensorMap& map_w, const CUtensorMap& map_x, AdapterArgs 
 }
 
 }  // namespace
+
+int launch_adapter_low_rows(const void* x, const void* wa, const AdapterArgs& a, cudaStream_t st)
+{
+    const long long warps = static_cast<long long>(a.T) * ((a.rank + 3) / 4);
+    const int grid = persistent_grid(reinterpret_cast<const void*>(&k_adapter_low_rows), 256, 0, (warps + 7) / 8);
+    if (grid < 1) return cudaErrorLaunchOutOfResources;
+    return launch_kernel(&k_adapter_low_rows, dim3(grid), dim3(256), 0, st, 0, static_cast<const __nv_bfloat16*>(x),
+                         static_cast<const __nv_bfloat16*>(wa), a);
+}
+
+int launch_adapter_few(const void* x, const void* w, bool f32, const AdapterArgs& a, cudaStream_t st)
+{
+    using B = __nv_bfloat16;
+    const size_t smem = static_cast<size_t>(a.T) * a.K * 2;
+    auto go = [&](auto kernel) -> int {
+        const void* f = reinterpret_cast<const void*>(kernel);
+        const int e = ensure_smem(f, smem);
+        if (e != cudaSuccess) return e;
+        const int grid = persistent_grid(f, 256, smem, (a.N + 7) / 8);
+        if (grid < 1) return cudaErrorLaunchOutOfResources;
+        return launch_kernel(kernel, dim3(grid), dim3(256), smem, st, 0, static_cast<const B*>(x), static_cast<const B*>(w), a);
+    };
+    if (a.T == 1) return f32 ? go(&k_adapter_few<1, float>) : go(&k_adapter_few<1, B>);
+    if (a.T == 2) return f32 ? go(&k_adapter_few<2, float>) : go(&k_adapter_few<2, B>);
+    return f32 ? go(&k_adapter_few<4, float>) : go(&k_adapter_few<4, B>);
+}
 
 int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_x, const AdapterArgs& a, int groups,
                        cudaStream_t st)

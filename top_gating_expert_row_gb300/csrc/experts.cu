@@ -237,13 +237,16 @@ size_t part(size_t& o, size_t bytes)
     return at;
 }
 
-// Columns (pairs) of a block: twice the mean load of an expert that has any, so
+// Units that keep the SMs busy (one CTA each).
+constexpr int kFullGrid = 148;
+
+// Columns (pairs) of a block: four times the mean load of an expert that has any, so
 // that few experts need a second block (which reads their weights again). A
 // product only takes the columns that its block fills, so wide blocks cost
 // shared memory, not time.
 int columns_for(long long P, int E)
 {
-    const long long load = 2 * ((P + std::min<long long>(P, E) - 1) / std::min<long long>(P, E));
+    const long long load = 4 * ((P + std::min<long long>(P, E) - 1) / std::min<long long>(P, E));
     int nt = 16;
     while (nt < 256 && nt < load) nt *= 2;
     return nt;
@@ -253,7 +256,7 @@ int columns_for(long long P, int E)
 int rows_for(long long blocks, int width, int per_row)
 {
     int rows = 128;
-    while (rows > 32 && blocks * ((static_cast<long long>(width) * per_row + rows - 1) / rows) < 148) rows /= 2;
+    while (rows > 32 && blocks * ((static_cast<long long>(width) * per_row + rows - 1) / rows) < kFullGrid) rows /= 2;
     return rows;
 }
 
@@ -406,21 +409,33 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
 struct AdapterPlan {
     size_t bytes;
     int nt, tiles, rows, mt, slices, groups;
+    bool low_rows;
 };
+
+// Rank-space values: up to this many products a warp per four of them, above
+// it the tensor cores.
+constexpr long long kLowRowsProducts = 64ll << 20;
+// Tokens that the projection on the CUDA cores takes, and their shared memory.
+constexpr int kFewProjTokens = 4;
 
 AdapterPlan adapter_plan(const mr_adapter_params& p)
 {
     AdapterPlan w;
+    // wide tiles of tokens read w less often; narrower ones while wide ones
+    // leave SMs without a unit
     w.nt = 16;
-    while (w.nt < 256 && w.nt < p.T) w.nt *= 2;
+    while (w.nt < 64 && w.nt < p.T) w.nt *= 2;
+    const long long mt = (p.N + 127) / 128;
+    while (w.nt >= 64 && w.nt < 256 && (p.T + 2 * w.nt - 1) / (2 * w.nt) * mt >= kFullGrid) w.nt *= 2;
     w.tiles = (p.T + w.nt - 1) / w.nt;
     w.rows = rows_for(w.tiles, p.N, 1);
     w.mt = (p.N + w.rows - 1) / w.rows;
     w.slices = 1;
     w.groups = 1;
     w.bytes = 0;
+    w.low_rows = static_cast<long long>(p.T) * p.rank * p.K <= kLowRowsProducts;
     if (p.n_adapters == 0) return w;
-    if (p.rank <= 128) {
+    if (p.rank <= 128 && !w.low_rows) {
         // as many CTAs as SMs or a little fewer: groups of adapters first (as
         // many as the tile's tokens can name), then slices of K
         const int distinct = std::min(std::min(w.nt, p.T), p.n_adapters);
@@ -585,7 +600,8 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
     const AdapterPlan plan = adapter_plan(*p);
     if (adapter_tensor_path(*p, plan, x, w, a, b)) {
         CUtensorMap mapw, mapx, mapa;
-        if (!encode_map(&mapw, w, p->K, p->N, 0, plan.rows) || !encode_map(&mapx, x, p->K, p->T, 0, plan.nt))
+        const bool few = p->T <= kFewProjTokens && plan.low_rows && static_cast<size_t>(p->T) * p->K * 2 <= kFewSmem;
+        if (!few && (!encode_map(&mapw, w, p->K, p->N, 0, plan.rows) || !encode_map(&mapx, x, p->K, p->T, 0, plan.nt)))
             return MR_ECUDA;
         AdapterArgs d;
         d.b = static_cast<const B*>(b);
@@ -605,10 +621,13 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
         d.mt = plan.mt;
         d.slices = plan.slices;
         wait_test(&d.tries, &d.drop);
-        if (p->n_adapters > 0) {
+        if (p->n_adapters > 0 && plan.low_rows) {
+            if (launch_adapter_low_rows(x, a, d, st) != cudaSuccess) return MR_ECUDA;
+        } else if (p->n_adapters > 0) {
             if (!encode_map(&mapa, a, p->K, p->rank, p->n_adapters, p->rank)) return MR_ECUDA;
             if (launch_adapter_low(plan.nt, mapa, mapx, d, plan.groups, st) != cudaSuccess) return MR_ECUDA;
         }
+        if (few) return from_cuda(launch_adapter_few(x, w, p->out_dtype == MR_F32, d, st));
         return from_cuda(launch_adapter_proj(plan.nt, p->out_dtype == MR_F32, mapw, mapx, d, st));
     }
     const long long T = p->T;

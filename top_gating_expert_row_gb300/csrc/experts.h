@@ -45,7 +45,7 @@ struct ExpertArgs {
 };
 
 // Blocks of this many pairs or more read x from a copy in sorted order.
-constexpr int kGatherColumns = 64;
+constexpr int kGatherColumns = 32;
 // Rows of one copy of the token operand.
 inline int token_box(int nt) { return nt >= 64 ? nt / 4 : 16; }
 
@@ -74,6 +74,8 @@ struct AdapterArgs {
 
 int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_x, const AdapterArgs& a, int groups,
                        cudaStream_t st);
+int launch_adapter_low_rows(const void* x, const void* wa, const AdapterArgs& a, cudaStream_t st);
+int launch_adapter_few(const void* x, const void* w, bool f32, const AdapterArgs& a, cudaStream_t st);
 int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const AdapterArgs& a,
                         cudaStream_t st);
 

@@ -98,7 +98,23 @@ __device__ __forceinline__ void few_up(const FewArgs& a, const int32_t* s_idx, c
     }
 }
 
-// Weights of this warp's first rows of `down`, to L2.
+// This warp's weights of `up`, to L2 at once: a warp holds one row pair's
+// loads in flight and has a few of them one after the other.
+__device__ __forceinline__ void few_up_prefetch(const FewArgs& a, const int32_t* s_idx)
+{
+    const int lane = threadIdx.x & 31, warps = gridDim.x * kFewWarps;
+    const long long first = static_cast<long long>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5);
+    // lanes 0, 1: the first row pair is loaded at once; from lane 2 on, the next ones
+    const long long u = first + static_cast<long long>(lane >> 1) * warps;
+    if (lane >= 2 && u < static_cast<long long>(a.T) * a.topk * a.I) {
+        const int p = static_cast<int>(u / a.I), i = static_cast<int>(u - static_cast<long long>(p) * a.I);
+        const int e = s_idx[p];
+        if (e >= 0 && e < a.E)
+            prefetch_l2(a.w13 + (static_cast<long long>(e) * 2 * a.I + i + (lane & 1 ? a.I : 0)) * a.H, a.H * 2);
+    }
+}
+
+// This warp's weights of `down`, to L2.
 __device__ __forceinline__ void few_down_prefetch(const FewArgs& a, const int32_t* s_idx)
 {
     const int lane = threadIdx.x & 31, warps = gridDim.x * kFewWarps;
@@ -121,32 +137,26 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const int32_t* s_idx,
     for (long long u = static_cast<long long>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5); u < static_cast<long long>(a.T) * a.H;
          u += warps) {
         const int t = static_cast<int>(u / a.H), c = static_cast<int>(u - static_cast<long long>(t) * a.H);
-        // the token's slots one after the other, as one row of topk * I
-        int j = 0, at = lane;
+        // the token's slots one after the other: step q is piece q % n of slot q / n
+        const int n = (I8 + 31) / 32, steps = a.topk * n;
+        int j = 0, piece = 0;
         float sum = 0.0f;
-        while (at >= I8 && j < a.topk) {
-            at -= I8;
-            ++j;
-        }
-        while (__any_sync(kFull, j < a.topk)) {
+        for (int q = 0; q < steps; q += kChunks) {
             uint4 w[kChunks];
             int src[kChunks];
             float weight[kChunks];
 #pragma unroll
             for (int k = 0; k < kChunks; ++k) {
-                src[k] = -1;
-                if (j < a.topk) {
-                    const int p = t * a.topk + j, e = s_idx[p];
-                    if (e >= 0 && e < a.E) {
-                        src[k] = p * I8 + at;
-                        weight[k] = s_w[p];
-                        w[k] = load_weights(reinterpret_cast<const uint4*>(a.w2 + (static_cast<long long>(e) * a.H + c) * a.I) + at);
-                    }
-                    at += 32;
-                    while (at >= I8 && j < a.topk) {
-                        at -= I8;
-                        ++j;
-                    }
+                const int at = piece * 32 + lane, p = t * a.topk + j;
+                const int e = q + k < steps ? s_idx[p] : -1;
+                src[k] = e >= 0 && e < a.E && at < I8 ? p * I8 + at : -1;
+                if (src[k] >= 0) {
+                    weight[k] = s_w[p];
+                    w[k] = load_weights(reinterpret_cast<const uint4*>(a.w2 + (static_cast<long long>(e) * a.H + c) * a.I) + at);
+                }
+                if (++piece == n) {
+                    piece = 0;
+                    ++j;
                 }
             }
 #pragma unroll
@@ -181,6 +191,7 @@ __device__ __forceinline__ void few_body(const FewArgs& a, unsigned char* smem, 
     choose(s_idx, s_w);
     __syncthreads();
     if (!DOWN) {
+        few_up_prefetch(a, s_idx);
         few_up(a, s_idx, s_v);
     } else {
         few_down_prefetch(a, s_idx);
