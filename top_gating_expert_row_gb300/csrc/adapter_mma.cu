@@ -236,36 +236,39 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 }
 
 // The same without tiles, for calls whose products are few: a warp takes four
-// ranks of one token, and a's rows come from L2 again for each token.
+// ranks of one token over a slice of K, and a's rows come from L2 again for
+// each token.
 __global__ void __launch_bounds__(256) k_adapter_low_rows(const __nv_bfloat16* x, const __nv_bfloat16* wa, AdapterArgs a)
 {
     pdl_wait();
     pdl_trigger();
     constexpr int kAtOnce = 4;
-    const int lane = threadIdx.x & 31, K8 = a.K / 8, quads = (a.rank + 3) / 4;
+    const int lane = threadIdx.x & 31, K8 = a.K / 8, quads = a.rank / 4;
+    const int part = (K8 + a.slices - 1) / a.slices;
     const long long warps = static_cast<long long>(gridDim.x) * 8;
-    for (long long u = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < static_cast<long long>(a.T) * quads;
+    for (long long u = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < static_cast<long long>(a.T) * quads * a.slices;
          u += warps) {
-        const long long t = u / quads;
-        const int r0 = static_cast<int>(u - t * quads) * 4;
+        const long long v = u / a.slices, t = v / quads;
+        const int slice = static_cast<int>(u - v * a.slices), r0 = static_cast<int>(v - t * quads) * 4;
+        const int end = min(K8, (slice + 1) * part);
         const int id = __ldcg(a.adapter + t);
-        if (id >= a.n_adapters && r0 == 0 && lane == 0) report_status(a.range_status, kStatusRange);
+        if (id >= a.n_adapters && r0 == 0 && slice == 0 && lane == 0) report_status(a.range_status, kStatusRange);
         if (id < 0 || id >= a.n_adapters) continue;
         const uint4* xr = reinterpret_cast<const uint4*>(x + t * a.K);
         const uint4* ar = reinterpret_cast<const uint4*>(wa + (static_cast<long long>(id) * a.rank + r0) * a.K);
         float sum[4] = {0, 0, 0, 0};  // rank is a multiple of 8: all four rows are there
-        for (int c0 = lane; c0 < K8; c0 += 32 * kAtOnce) {
+        for (int c0 = slice * part + lane; c0 < end; c0 += 32 * kAtOnce) {
             uint4 xc[kAtOnce], ac[kAtOnce][4];
 #pragma unroll
             for (int c = 0; c < kAtOnce; ++c)
-                if (c0 + c * 32 < K8) {
+                if (c0 + c * 32 < end) {
                     xc[c] = __ldcg(xr + c0 + c * 32);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) ac[c][q] = __ldcg(ar + static_cast<long long>(q) * K8 + c0 + c * 32);
                 }
 #pragma unroll
             for (int c = 0; c < kAtOnce; ++c)
-                if (c0 + c * 32 < K8) {
+                if (c0 + c * 32 < end) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) sum[q] = dot8(ac[c][q], xc[c], sum[q]);
                 }
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(256) k_adapter_low_rows(const __nv_bfloat16* x
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const float v = warp_sum(sum[q]);
-            if (lane == q) a.low[t * a.rank + r0 + q] = v * sc;
+            if (lane == q) a.low[(static_cast<long long>(slice) * a.T + t) * a.rank + r0 + q] = v * sc;
         }
     }
 }
@@ -288,6 +291,7 @@ __global__ void __launch_bounds__(256) k_adapter_few(const __nv_bfloat16* x, con
     extern __shared__ __align__(16) unsigned char smem[];
     const bool low = a.n_adapters > 0;
     if (!low) pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, K8 = a.K / 8;
     for (int i = threadIdx.x; i < a.T * K8; i += 256)
         reinterpret_cast<uint4*>(smem)[i] = __ldcg(reinterpret_cast<const uint4*>(x) + i);
@@ -329,8 +333,11 @@ __global__ void __launch_bounds__(256) k_adapter_few(const __nv_bfloat16* x, con
                 if (id[t] < 0) continue;
                 const __nv_bfloat16* br = a.b + (static_cast<long long>(id[t]) * a.N + row) * a.rank;
                 const float* s = a.low + static_cast<long long>(t) * a.rank;
-                if (lane < a.rank) sum[t] = fmaf(b0[t], __ldcg(s + lane), sum[t]);
-                for (int r = lane + 32; r < a.rank; r += 32) sum[t] = fmaf(load_scalar(br + r), __ldcg(s + r), sum[t]);
+                for (int r = lane; r < a.rank; r += 32) {
+                    float v = 0.0f;
+                    for (int p = 0; p < a.slices; ++p) v += __ldcg(s + static_cast<long long>(p) * a.T * a.rank + r);
+                    sum[t] = fmaf(r == lane ? b0[t] : load_scalar(br + r), v, sum[t]);
+                }
             }
         }
 #pragma unroll
@@ -404,6 +411,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // trigger comes after its own wait, x and w are there already.
     const bool low = a.n_adapters > 0;
     if (!low) pdl_wait();
+    pdl_trigger();
 
     const Waits wait{&bars.gone, a.tries};
     const uint32_t drain = min(a.tries, kDrainTries);
@@ -666,7 +674,7 @@ int launch_proj(const CUtensorMap& map_w, const CUtensorMap& map_x, AdapterArgs 
 
 int launch_adapter_low_rows(const void* x, const void* wa, const AdapterArgs& a, cudaStream_t st)
 {
-    const long long warps = static_cast<long long>(a.T) * ((a.rank + 3) / 4);
+    const long long warps = static_cast<long long>(a.T) * (a.rank / 4) * a.slices;
     const int grid = persistent_grid(reinterpret_cast<const void*>(&k_adapter_low_rows), 256, 0, (warps + 7) / 8);
     if (grid < 1) return cudaErrorLaunchOutOfResources;
     return launch_kernel(&k_adapter_low_rows, dim3(grid), dim3(256), 0, st, 0, static_cast<const __nv_bfloat16*>(x),

@@ -226,7 +226,7 @@ int check_adapter(const mr_adapter_params* p)
 // Workspace of the experts' products: offsets of its parts. The plain kernels
 // use idx, w and h alone.
 struct ExpertPlan {
-    size_t idx, w, h, xs, sids, eids, npp, count, y, sort, sort_bytes, bytes;
+    size_t idx, w, h, xs, sids, eids, npp, y, sort, sort_bytes, bytes;
     int nt, cap, rows_up, rows_down, mt_up, mt_down;
 };
 
@@ -281,7 +281,6 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     w.sids = part(o, cap * 4);
     w.eids = part(o, (cap / w.nt + 1) * 4);
     w.npp = part(o, 4);
-    w.count = part(o, static_cast<size_t>(p.T) * w.mt_down * 4);
     w.sort_bytes = moe_sort_workspace_bytes(p.T, p.topk, p.E, w.nt);
     if (route) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
     w.sort = part(o, w.sort_bytes);
@@ -371,7 +370,7 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     ExpertArgs a;
     a.x = static_cast<const __nv_bfloat16*>(x);
     a.xs = reinterpret_cast<__nv_bfloat16*>(ws + plan.xs);
-    a.out8 = aligned(out, 8);
+    a.out16 = aligned(out, 16);
     a.sids = reinterpret_cast<int32_t*>(ws + plan.sids);
     a.eids = reinterpret_cast<int32_t*>(ws + plan.eids);
     a.npp = reinterpret_cast<int32_t*>(ws + plan.npp);
@@ -379,7 +378,6 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     a.w = w;
     a.h = reinterpret_cast<__nv_bfloat16*>(ws + plan.h);
     a.y = reinterpret_cast<float*>(ws + plan.y);
-    a.count = reinterpret_cast<int32_t*>(ws + plan.count);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.status = status_word(status);
     a.T = p.T;
@@ -390,7 +388,6 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     a.P = p.T * p.topk;
     a.cap = plan.cap;
     a.act = p.act;
-    a.mt_down = plan.mt_down;
     wait_test(&a.tries, &a.drop);
     const long long blocks = plan.cap / plan.nt;
     a.rows = plan.rows_up;
@@ -401,7 +398,8 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     if (e != cudaSuccess) return MR_ECUDA;
     a.rows = plan.rows_down;
     a.mt = plan.mt_down;
-    return from_cuda(launch_experts_down(plan.nt, map2, maph, a, blocks * a.mt, st));
+    e = launch_experts_down(plan.nt, map2, maph, a, blocks * a.mt, st);
+    return e != cudaSuccess ? MR_ECUDA : from_cuda(launch_experts_sum(a, st));
 }
 
 // Workspace of the adapter projection (the rank-space values; the plain kernels
@@ -435,7 +433,11 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
     w.bytes = 0;
     w.low_rows = static_cast<long long>(p.T) * p.rank * p.K <= kLowRowsProducts;
     if (p.n_adapters == 0) return w;
-    if (p.rank <= 128 && !w.low_rows) {
+    if (w.low_rows) {
+        // slices of K while there are fewer warps than the SMs hold in flight
+        const long long warps = static_cast<long long>(p.T) * ((p.rank + 3) / 4);
+        while (w.slices < 8 && warps * w.slices < 1024 && p.K / (w.slices * 2) >= 512) w.slices *= 2;
+    } else if (p.rank <= 128) {
         // as many CTAs as SMs or a little fewer: groups of adapters first (as
         // many as the tile's tokens can name), then slices of K
         const int distinct = std::min(std::min(w.nt, p.T), p.n_adapters);

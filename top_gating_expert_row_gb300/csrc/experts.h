@@ -32,15 +32,13 @@ struct ExpertArgs {
     const float* w;        // [T][topk]
     __nv_bfloat16* h;      // [cap][I], in sorted order
     float* y;              // [T * topk][H], weighted
-    int32_t* count;        // [T][mt_down] slots done
     __nv_bfloat16* out;    // [T][H]
     int32_t* status;
     int T, topk, H, I, E, P, cap;
     int rows;              // weight rows of a stage (up: gate and up rows together)
     int mt;                // row tiles of this kernel
-    int mt_down;           // row tiles of `down`
     int stages, act, drop;
-    int out8;              // out allows 8-byte stores
+    int out16;             // out allows 16-byte stores
     uint32_t tries;
 };
 
@@ -50,6 +48,7 @@ constexpr int kGatherColumns = 32;
 inline int token_box(int nt) { return nt >= 64 ? nt / 4 : 16; }
 
 int launch_experts_gather(const ExpertArgs& a, cudaStream_t st);
+int launch_experts_sum(const ExpertArgs& a, cudaStream_t st);
 int launch_experts_up(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t, const ExpertArgs& a, long long units,
                       cudaStream_t st);
 int launch_experts_down(int nt, const CUtensorMap& map_w, const CUtensorMap& map_t, const ExpertArgs& a,

@@ -2,9 +2,10 @@
 // at most NT pairs of one expert).
 //
 //   k_experts_up    h[p][i] = act(w13[e][i] . x_t) * (w13[e][I + i] . x_t)
-//   k_experts_down  y[t][j] = weight * (w2[e] . h[p]), then out[t] = sum_j y[t][j]
+//   k_experts_down  y[t][j] = weight * (w2[e] . h[p])
+//   k_experts_sum   out[t] = sum_j y[t][j], in slot order
 //
-// Both are one persistent CTA per SM over units (block, row tile); see gemm.cuh
+// The first two are one persistent CTA per SM over units (block, row tile); see gemm.cuh
 // for the operands' roles. A unit of `up` holds rows/2 gate rows and the same
 // rows/2 up rows, alternating by 16, so that a warp of the epilogue has both
 // factors of h and one shuffle brings them together.
@@ -14,16 +15,16 @@
 // engine 80 clocks, of 64 consecutive rows 120, and each row tile of w13 reads
 // the block's rows again.
 //
-// The sum over a token's slots is taken in slot order by whichever unit
-// completes the token's last slot (a counter per token and row tile): the same
-// bits whatever the order of arrival, and no launch for it.
+// The sum over a token's slots is a kernel of its own. Taken by the unit that
+// completes a token (a counter per token and row tile), it cost `down` a fence,
+// an atomic and a fence a unit, 4 us of latency that the next unit's products
+// did not cover (T=16 E=256 k=8: 83 us instead of 60; T=8192 E=8 k=2: 208 us).
 #include "experts.h"
 #include "gemm.cuh"
 
 namespace mr {
 
 namespace {
-constexpr int kTokensAtOnce = 4;  // tokens a warp of the epilogue sums at a time: enough loads in flight
 template <int NT>
 constexpr int kTokenBox = NT >= 64 ? NT / 4 : 16;
 }  // namespace
@@ -42,7 +43,7 @@ __host__ __device__ inline CtaLayout cta_layout(int nt, int rows, int stages)
     // a product reads 128 rows from the start of a stage, also of the last one
     const uint32_t reach = static_cast<uint32_t>(stages - 1) * rows * kStepBytes + 128 * kStepBytes;
     if (o < reach) o = reach;
-    L.info = o; o += static_cast<uint32_t>(nt) * 12 + 16;
+    L.info = o; o += static_cast<uint32_t>(nt) * 8;
     o = (o + 15) / 16 * 16;
     L.bars = o; o += sizeof(GemmBars);
     L.bytes = o + 1024;  // the base is aligned inside
@@ -64,27 +65,7 @@ __device__ __forceinline__ int block_pairs(const int32_t* ids, int P, int lane)
     return n;
 }
 
-// The counters of `down`, the weighted products of slots without an expert and
-// the output rows of tokens without any; a warp per token.
-__device__ __forceinline__ void prepare_tokens(const ExpertArgs& a, int first, int warps, int lane)
-{
-    for (int t = first; t < a.T; t += warps) {
-        int none = 0;
-        for (int j = 0; j < a.topk; ++j) {
-            const long long pair = static_cast<long long>(t) * a.topk + j;
-            const int e = __ldcg(a.idx + pair);
-            if (e >= 0 && e < a.E) continue;
-            ++none;
-            for (int c = lane * 4; c < a.H; c += 128)
-                *reinterpret_cast<float4*>(a.y + pair * a.H + c) = make_float4(0, 0, 0, 0);
-        }
-        for (int m = lane; m < a.mt_down; m += 32) a.count[static_cast<long long>(t) * a.mt_down + m] = none;
-        if (none == a.topk)
-            for (int c = lane; c < a.H; c += 32) a.out[static_cast<long long>(t) * a.H + c] = __float2bfloat16_rn(0.0f);
-    }
-}
-
-// xs[r] = x[token of sorted row r], and prepare_tokens; a warp per row.
+// xs[r] = x[token of sorted row r]; a warp per row.
 __global__ void __launch_bounds__(256) k_experts_gather(const __grid_constant__ ExpertArgs a)
 {
     pdl_wait();
@@ -99,7 +80,45 @@ __global__ void __launch_bounds__(256) k_experts_gather(const __grid_constant__ 
 #pragma unroll 4
         for (int c = lane; c < a.H / 8; c += 32) dst[c] = __ldcg(src + c);
     }
-    prepare_tokens(a, warp, warps, lane);
+}
+
+// out[t] = sum of the token's weighted products in slot order (zeros where no
+// slot has an expert); a thread takes 8 columns of a token.
+__global__ void __launch_bounds__(256) k_experts_sum(const __grid_constant__ ExpertArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int H8 = a.H / 8;
+    const long long n = static_cast<long long>(a.T) * H8;
+    for (long long u = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; u < n; u += static_cast<long long>(gridDim.x) * 256) {
+        const long long t = u / H8;
+        const int c = static_cast<int>(u - t * H8) * 8;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+        for (int j = 0; j < a.topk; ++j) {
+            const long long pair = t * a.topk + j;
+            const int e = __ldcg(a.idx + pair);
+            const float4* y = reinterpret_cast<const float4*>(a.y + pair * a.H + c);
+            const float4 p = __ldcs(y), q = __ldcs(y + 1);  // of a slot without an expert: whatever is there
+            if (e >= 0 && e < a.E) {
+                v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+                v[4] += q.x; v[5] += q.y; v[6] += q.z; v[7] += q.w;
+            }
+        }
+        __nv_bfloat16* o = a.out + t * a.H + c;
+        if (a.out16) {
+            uint4 w;
+            uint32_t* wp = &w.x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                wp[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(o) = w;
+        } else {
+            for (int i = 0; i < 8; ++i) o[i] = __float2bfloat16_rn(v[i]);
+        }
+    }
 }
 
 template <int NT, bool DOWN>
@@ -138,11 +157,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     // `up` follows the sort and lets `down` start; `down` knows then that the
     // sort is done (up's trigger comes after up's own wait) and may fetch
-    // weights before `up` ends.
-    if (!DOWN) {
-        pdl_wait();
-        pdl_trigger();
-    }
+    // weights before `up` ends. Every kernel after them waits before it reads.
+    if (!DOWN) pdl_wait();
+    pdl_trigger();
     const Waits wait{&bars.gone, a.tries};
     const uint32_t drain = min(a.tries, kDrainTries);
     const int nblk = min(__ldcg(a.npp), a.cap) / NT;
@@ -263,11 +280,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp >= 4) {
         const int et = threadIdx.x - kEpilogueThreads, q = warp - 4;  // this thread's row of the accumulator
         if (DOWN) pdl_wait();
-        if (!DOWN && NT < kGatherColumns) prepare_tokens(a, blockIdx.x * 4 + q, gridDim.x * 4, lane);
-        int* info = reinterpret_cast<int*>(smem + L.info);  // NT pair ids, NT weights, NT completed tokens and their number
+        int* info = reinterpret_cast<int*>(smem + L.info);  // NT pair ids, NT weights
         float* info_w = reinterpret_cast<float*>(info + NT);
-        int* done = info + 2 * NT;
-        int* ndone = info + 3 * NT;
         int seen = 0;
         for (int u = blockIdx.x; u < units; u += gridDim.x, ++seen) {
             const int b = u / a.mt, m = u - b * a.mt, buf = seen & 1;
@@ -279,7 +293,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     info[c] = id;
                     info_w[c] = __ldcg(a.w + id);
                 }
-                if (et == 0) *ndone = 0;
             }
             if (!epilogue_wait(wait, &bars.acc_full[buf], (seen >> 1) & 1)) break;
             tc_fence_after();
@@ -297,46 +310,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 tc_fence_before();
                 mbar_arrive(&bars.acc_empty[buf]);
-                // this unit's products before its counts, everyone's counts before their products
-                __threadfence();
-                epilogue_sync();
-                for (int c = et; c < n; c += kEpilogueThreads) {
-                    const int t = info[c] / a.topk;
-                    if (atomicAdd(a.count + static_cast<long long>(t) * a.mt_down + m, 1) == a.topk - 1)
-                        done[atomicAdd(ndone, 1)] = t;
-                }
-                __threadfence();
-                epilogue_sync();
-                // four rows a lane; tokens side by side where the tile has fewer than 128 rows
-                const int lanes = a.rows >> 2, per_warp = 32 / lanes, r = m * a.rows + (lane % lanes) * 4;
-                const int nd = *ndone;
-                if (r < a.H)
-                    for (int i = q * per_warp + lane / lanes; i < nd; i += 4 * per_warp * kTokensAtOnce) {
-                        float4 sum[kTokensAtOnce];
-                        const float* y[kTokensAtOnce];
-#pragma unroll
-                        for (int k = 0; k < kTokensAtOnce; ++k) {
-                            const int at = min(i + k * 4 * per_warp, nd - 1);
-                            y[k] = a.y + static_cast<long long>(done[at]) * a.topk * a.H + r;
-                            sum[k] = make_float4(0, 0, 0, 0);
-                        }
-#pragma unroll 2
-                        for (int j = 0; j < a.topk; ++j)
-#pragma unroll
-                            for (int k = 0; k < kTokensAtOnce; ++k) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(y[k] + static_cast<long long>(j) * a.H));
-                                sum[k].x += v.x; sum[k].y += v.y; sum[k].z += v.z; sum[k].w += v.w;
-                            }
-#pragma unroll
-                        for (int k = 0; k < kTokensAtOnce; ++k)
-                            if (i + k * 4 * per_warp < nd) {
-                                const float v[4] = {sum[k].x, sum[k].y, sum[k].z, sum[k].w};
-                                __nv_bfloat16* o = a.out + static_cast<long long>(done[i + k * 4 * per_warp]) * a.H + r;
-                                if (a.out8) store4(o, v);
-                                else
-                                    for (int z = 0; z < 4; ++z) o[z] = __float2bfloat16_rn(v[z]);
-                            }
-                    }
                 epilogue_sync();  // the next unit overwrites info
             } else {
                 // lanes 0-15 hold gate rows, lanes 16-31 the same up rows: the
@@ -377,6 +350,14 @@ int launch_experts_gather(const ExpertArgs& a, cudaStream_t st)
     const int grid = persistent_grid(reinterpret_cast<const void*>(&k_experts_gather), 256, 0, (a.cap + 7) / 8);
     if (grid < 1) return cudaErrorLaunchOutOfResources;
     return launch_kernel(&k_experts_gather, dim3(grid), dim3(256), 0, st, 0, a);
+}
+
+int launch_experts_sum(const ExpertArgs& a, cudaStream_t st)
+{
+    const long long n = static_cast<long long>(a.T) * (a.H / 8);
+    const int grid = persistent_grid(reinterpret_cast<const void*>(&k_experts_sum), 256, 0, (n + 255) / 256);
+    if (grid < 1) return cudaErrorLaunchOutOfResources;
+    return launch_kernel(&k_experts_sum, dim3(grid), dim3(256), 0, st, 0, a);
 }
 
 namespace {

@@ -195,6 +195,7 @@ __device__ __forceinline__ void few_body(const FewArgs& a, unsigned char* smem, 
         few_up(a, s_idx, s_v);
     } else {
         few_down_prefetch(a, s_idx);
+        pdl_trigger();
         pdl_wait();
         few_stage(s_v, a.h, P * a.I / 8);
         __syncthreads();
