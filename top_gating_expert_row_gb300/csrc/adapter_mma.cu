@@ -6,21 +6,30 @@
 //
 // Tokens are taken in tiles of at most NT and need no sorting by adapter.
 //
-// The second part of k_adapter_proj, rank multiply-adds an output, is taken by
-// the epilogue warps in fp32 while the tensor cores sum over K: each token's
-// with its own b[i] only. (As further columns of the tensor cores' sum, the
-// tokens of other adapters would meet b[i] with zeros, and an infinity in one
-// request's adapter would reach every token of the tile.)
+// The second part of k_adapter_proj, rank multiply-adds an output:
+// * A wide tile (128 or 256 tokens) whose tokens all name the same adapter, the
+//   usual one of a prompt, takes it as further steps of the tensor cores' sum,
+//   with s as two bf16 parts (s = hi + lo to 16 significant bits, made by
+//   k_adapter_split) against the same b[i]: 2 steps of 66 at rank 64, K 4096,
+//   where the epilogue's multiply-adds took three times the products' time.
+// * Otherwise the epilogue warps take it in fp32, each token's with its own
+//   b[i] only. (In the tensor cores' sum the tokens of other adapters would meet
+//   b[i] with zeros, and an infinity in one request's adapter would reach every
+//   token of the tile.) In narrow tiles that is done before the sum over K is.
 //
 // k_adapter_proj starts while k_adapter_low runs (its sum over K needs nothing
 // of it), so the low-rank product costs little time of its own once w is large.
+#include <type_traits>
+
 #include "few.cuh"
 #include "gemm.cuh"
 
 namespace mr {
 
 namespace {
-constexpr int kSmallTile = 64;  // tiles up to this keep the adapters' part of a whole unit in shared memory
+constexpr int kChunkRanks = 32;  // ranks of a further step (hi and lo)
+constexpr int kSegment = 8;      // k-steps between readings of the accumulator, fp32 output
+constexpr int kSmallTile = 64;   // tiles up to this keep the adapters' part of a whole unit in shared memory
 
 struct AdapterLayout {
     uint32_t a, b, ids, list, low, part, bars, bytes;
@@ -68,6 +77,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int* slot = reinterpret_cast<int*>(smem + L.ids);    // token -> place in the list, -1: none
     int* list = reinterpret_cast<int*>(smem + L.list);   // the tile's distinct adapters, by first appearance
     int* count = list + NT;
+    __shared__ int warp_first[kGemmThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr uint32_t kColumns = 2 * NT;
     const int group = 128 / a.rank;
@@ -86,7 +96,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         mbar_init(&bars.drained, 1);
         bars.gone = 0;
-        *count = 0;
         prefetch_map(&map_a);
         prefetch_map(&map_x);
     }
@@ -99,32 +108,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         slot[t] = id >= 0 && id < a.n_adapters ? id : -1;
     }
     __syncthreads();
-    int id = -1, first = -1;
+    // a token is its adapter's first if no earlier one names it (the previous
+    // one does, mostly); the first ones are listed in order
+    int id = -1;
+    bool first = false;
     if (threadIdx.x < NT) {
         id = slot[threadIdx.x];
-        if (id >= 0) {
-            first = threadIdx.x;
-            for (int t = 0; t < static_cast<int>(threadIdx.x); ++t)
-                if (slot[t] == id) {
-                    first = t;
-                    break;
-                }
-        }
+        first = id >= 0;
+        for (int t = static_cast<int>(threadIdx.x) - 1; first && t >= 0; --t) first = slot[t] != id;
     }
+    const uint32_t firsts = __ballot_sync(kFull, first);
+    if (lane == 0) warp_first[warp] = __popc(firsts);
     __syncthreads();
-    // the place of a first appearance: how many there are before it
-    if (threadIdx.x < NT) list[threadIdx.x] = first == static_cast<int>(threadIdx.x);
-    __syncthreads();
-    int place = -1;
-    if (first >= 0) {
-        place = 0;
-        for (int t = 0; t < first; ++t) place += list[t];
-    }
-    __syncthreads();
-    if (threadIdx.x < NT) slot[threadIdx.x] = place;
-    if (first == static_cast<int>(threadIdx.x) && id >= 0) {
+    if (first) {
+        int place = __popc(firsts & lanemask_lt());
+        for (int w = 0; w < warp; ++w) place += warp_first[w];
         list[place] = id;
-        atomicAdd(count, 1);
+    }
+    if (threadIdx.x == 0) {
+        int n = 0;
+        for (int w = 0; w < kGemmThreads / 32; ++w) n += warp_first[w];
+        *count = n;
+    }
+    __syncthreads();
+    if (id >= 0) {
+        int place = 0;
+        while (list[place] != id) ++place;
+        slot[threadIdx.x] = place;
     }
     tc_fence_before();
     __syncthreads();
@@ -374,16 +384,69 @@ __device__ __forceinline__ void unpack8(uint4 p, float (&v)[8])
     }
 }
 
+// hi and lo of 8 consecutive ranks, packed; an infinity has no remainder.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        h[i] = *reinterpret_cast<const uint32_t*>(&p);
+        const float x = __low2float(p), y = __high2float(p);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(isinf(x) ? 0.0f : v[2 * i] - x, isinf(y) ? 0.0f : v[2 * i + 1] - y);
+        l[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// Wide tiles: whether all tokens of the tile name one adapter, and if so their
+// rank-space values as the token operand of k_adapter_proj's further steps.
+// Grid: tiles by 8 parts of a tile.
+template <int NT>
+__global__ void __launch_bounds__(256) k_adapter_split(AdapterArgs a)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int t0 = blockIdx.x * NT, tokens = min(NT, a.T - t0);
+    const int ad = __ldcg(a.adapter + t0);
+    const int mine = static_cast<int>(threadIdx.x) < tokens ? __ldcg(a.adapter + t0 + threadIdx.x) : ad;
+    const bool same = __syncthreads_and(mine == ad) && ad >= 0 && ad < a.n_adapters;
+    if (blockIdx.y == 0 && threadIdx.x == 0) a.same[blockIdx.x] = same ? ad : -1;
+    if (!same) return;
+    const int octets = (a.rank + kChunkRanks - 1) / kChunkRanks * (kChunkRanks / 8), part = NT / 8;
+    for (int f = threadIdx.x; f < part * octets; f += 256) {
+        const int t = blockIdx.y * part + f / octets, o = f % octets;
+        if (t >= tokens) break;
+        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (o * 8 < a.rank) {
+            const float4 x = low4(a, t0 + t, o * 8), y = low4(a, t0 + t, o * 8 + 4);
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        }
+        uint4 hi, lo;
+        split8(v, hi, lo);
+        uint4* row = reinterpret_cast<uint4*>(a.split + (static_cast<long long>(t0 + t) * octets + o / 4 * 4) * 16);
+        row[o % 4] = hi;
+        row[4 + o % 4] = lo;
+    }
+}
+
+// Output in fp32: the tensor cores add to their accumulator without rounding
+// the last bit, off by 2e-6 of the result at K = 4096, so it is taken out every
+// kSegment steps and the parts are summed in registers (tiles of at most 64
+// tokens, whose sums fit there). In bf16 one segment does.
 template <int NT, typename OutT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_adapter_proj(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_s,
                    const __grid_constant__ AdapterArgs a)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const AdapterLayout L = adapter_layout(NT, a.rows, a.stages, a.n_adapters > 0 ? a.rank : 0);
     GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     constexpr uint32_t kColumns = 2 * NT;
     const uint32_t a_bytes = a.rows * kStepBytes, b_bytes = NT * kStepBytes;
     const uint32_t ring_a = smem_addr(smem + L.a), ring_b = smem_addr(smem + L.b);
@@ -421,21 +484,48 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     int issued = 0;
     bool ok = true;
 
+    constexpr bool kWide = NT > kSmallTile, kSegments = std::is_same<OutT, float>::value;
+    const int segments = kSegments ? (ksteps + kSegment - 1) / kSegment : 1;
+    const int chunks = (a.rank + kChunkRanks - 1) / kChunkRanks;  // further steps of a tile with one adapter
+    bool waited = !low;
+    // the adapter whose steps follow the sum over K, or -1; asked for at the
+    // unit's start once it is known by then
+    constexpr int kUnknown = -2;
+    auto early_adapter = [&](int b) { return !kWide || !low ? -1 : waited ? __ldcg(a.same + b) : kUnknown; };
+    auto one_adapter = [&](int b, int early) {
+        if (early != kUnknown) return early;
+        pdl_wait();
+        waited = true;
+        return __ldcg(a.same + b);
+    };
+
     if (warp == 0 || warp == 2) {
         if (elect_one()) {
             for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
                 const int b = u / a.mt, m = u - b * a.mt;
-                for (int k = 0; k < ksteps; ++k) {
+                int steps = ksteps, ad = early_adapter(b);
+                for (int k = 0; k < steps; ++k) {
                     ok = pos.wraps == 0 || wait(&bars.empty[pos.s], (pos.wraps - 1) & 1);
                     if (!ok) break;
                     uint64_t* full = &bars.full[pos.s];
                     mbar_expect(full, warp == 0 ? a_bytes : b_bytes);
                     ++issued;
                     if (!a.drop) {
-                        if (warp == 0) load_box2(ring_a + pos.s * a_bytes, &map_w, k * kStepK, m * a.rows, full);
-                        else load_box2(ring_b + pos.s * b_bytes, &map_x, k * kStepK, b * NT, full);
+                        const uint32_t dst = warp == 0 ? ring_a + pos.s * a_bytes : ring_b + pos.s * b_bytes;
+                        if (k < ksteps) {
+                            if (warp == 0) load_box2(dst, &map_w, k * kStepK, m * a.rows, full);
+                            else load_box2(dst, &map_x, k * kStepK, b * NT, full);
+                        } else {
+                            const int c = k - ksteps;
+                            if (warp == 0) load_box3(dst, &map_b, c * kChunkRanks, m * a.rows, ad, full);
+                            else load_box2(dst, &map_s, c * kStepK, b * NT, full);
+                        }
                     }
                     pos.next(a.stages);
+                    if (k == ksteps - 1) {
+                        ad = one_adapter(b, ad);
+                        if (ad >= 0) steps += chunks;
+                    }
                 }
             }
             if (!ok)
@@ -445,23 +535,46 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp == 1) {
         if (elect_one()) {
             int seen = 0;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++seen) {
-                const int b = u / a.mt, buf = seen & 1;
-                const uint32_t desc = product_desc((min(NT, a.T - b * NT) + 15) & ~15), d = tmem + buf * NT;
-                ok = seen < 2 || wait(&bars.acc_empty[buf], ((seen >> 1) - 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                for (int k = 0; k < ksteps; ++k) {
-                    ok = wait(&bars.full[pos.s], pos.wraps & 1);
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const int b = u / a.mt;
+                const uint32_t desc = product_desc((min(NT, a.T - b * NT) + 15) & ~15);
+                const int early = early_adapter(b);
+                for (int g = 0; ok && g < segments; ++g, ++seen) {
+                    const int buf = seen & 1, k1 = kSegments ? min(ksteps, (g + 1) * kSegment) : ksteps;
+                    const uint32_t d = tmem + buf * NT;
+                    ok = seen < 2 || wait(&bars.acc_empty[buf], ((seen >> 1) - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t da = operand_desc(ring_a + pos.s * a_bytes), db = operand_desc(ring_b + pos.s * b_bytes);
+                    bool add = false;
+                    for (int k = kSegments ? g * kSegment : 0; k < k1; ++k) {
+                        ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t da = operand_desc(ring_a + pos.s * a_bytes), db = operand_desc(ring_b + pos.s * b_bytes);
 #pragma unroll
-                    for (int q = 0; q < kStepK / 16; ++q) mma16(d, da + q * 2, db + q * 2, desc, k > 0 || q > 0);
-                    mma_commit(&bars.empty[pos.s]);
-                    pos.next(a.stages);
+                        for (int q = 0; q < kStepK / 16; ++q) {
+                            mma16(d, da + q * 2, db + q * 2, desc, add);
+                            add = true;
+                        }
+                        mma_commit(&bars.empty[pos.s]);
+                        pos.next(a.stages);
+                    }
+                    if (ok && one_adapter(b, early) >= 0)
+                        for (int c = 0; c < chunks; ++c) {
+                            ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t da = operand_desc(ring_a + pos.s * a_bytes), db = operand_desc(ring_b + pos.s * b_bytes);
+                            const int nq = (min(a.rank - c * kChunkRanks, kChunkRanks) + 15) / 16;
+                            for (int q = 0; q < nq; ++q) {
+                                mma16(d, da + q * 2, db + q * 2, desc, true);
+                                mma16(d, da + q * 2, db + (2 + q) * 2, desc, true);
+                            }
+                            mma_commit(&bars.empty[pos.s]);
+                            pos.next(a.stages);
+                        }
+                    if (ok) mma_commit(&bars.acc_full[buf]);
                 }
-                if (ok) mma_commit(&bars.acc_full[buf]);
             }
             if (!ok) {
                 mma_commit(&bars.drained);
@@ -477,8 +590,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int rank = a.rank, pitch = rank + 8;             // 16 bytes more a row: no bank conflicts
         if (low) pdl_wait();
         int seen = 0, tile = -1;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++seen) {
-            const int b = u / a.mt, m = u - b * a.mt, buf = seen & 1, t0 = b * NT, tokens = min(NT, a.T - t0);
+        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+            const int b = u / a.mt, m = u - b * a.mt, t0 = b * NT, tokens = min(NT, a.T - t0);
             const int row = m * a.rows + et;
             const bool there = et < a.rows && row < a.N;
             if (low) {
@@ -533,19 +646,53 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 tile = b;
             }
-            if (!epilogue_wait(wait, &bars.acc_full[buf], (seen >> 1) & 1)) break;
+            // the adapter's part is in the accumulator
+            const bool summed = kWide && low && __ldcg(a.same + b) >= 0;
+            // the parts of all segments but the last
+            float sum[kSegments ? NT : 1];
+            if (kSegments) {
+#pragma unroll
+                for (int c = 0; c < NT; ++c) sum[c] = 0.0f;
+                for (int g = 0; ok && g < segments - 1; ++g, ++seen) {
+                    ok = epilogue_wait(wait, &bars.acc_full[seen & 1], (seen >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c0 = 0; c0 < NT; c0 += 16)
+                        if (c0 < tokens) {
+                            float v[16];
+                            tmem_load16(tmem + (seen & 1) * NT + (static_cast<uint32_t>(q * 32) << 16) + c0, v);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) sum[c0 + c] += v[c];
+                        }
+                    tc_fence_before();
+                    mbar_arrive(&bars.acc_empty[seen & 1]);
+                }
+                if (!ok) break;
+            }
+            const int buf = seen & 1;
+            ok = epilogue_wait(wait, &bars.acc_full[buf], (seen >> 1) & 1);
+            if (!ok) break;
+            ++seen;
             tc_fence_after();
             const uint32_t acc = tmem + buf * NT + (static_cast<uint32_t>(q * 32) << 16);
             OutT* out = static_cast<OutT*>(a.out) + static_cast<long long>(t0) * a.N + row;
             int held = -1;  // the adapter whose rows are in rows_b
-            for (int c0 = 0; c0 < tokens; c0 += 16) {
+            constexpr int kUnroll = kSegments ? NT / 16 : 1;  // `sum` stays in registers
+#pragma unroll kUnroll
+            for (int c0 = 0; c0 < NT; c0 += 16) {
+                if (c0 >= tokens) continue;
                 float v[16];
                 tmem_load16(acc + c0, v);
+                if (kSegments) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] += sum[kSegments ? c0 + c : 0];
+                }
                 if (low && NT <= kSmallTile) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
                         if (et < a.rows && c0 + c < tokens) v[c] += part[(c0 + c) * a.rows + et];
-                } else if (low) {
+                } else if (low && !summed) {
                     const int ad = mine[c0];
                     bool same = true, any = false;
                     for (int c = 0; c < 16; ++c) {
@@ -635,7 +782,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
 namespace {
 
-// k_adapter_proj leaves room for a CTA of k_adapter_low beside it.
+// With narrow tiles k_adapter_proj leaves room for a CTA of k_adapter_low beside it.
 constexpr int kLowBudget = 60 * 1024, kProjBudget = 164 * 1024;
 
 int stages_for(int nt, int rows, int rank, int budget)
@@ -648,7 +795,7 @@ int stages_for(int nt, int rows, int rank, int budget)
 template <int NT>
 int launch_low(const CUtensorMap& map_a, const CUtensorMap& map_x, AdapterArgs a, int groups, cudaStream_t st)
 {
-    a.stages_low = stages_for(NT, 128, 0, kLowBudget);
+    a.stages_low = stages_for(NT, 128, 0, NT > kSmallTile ? kProjBudget : kLowBudget);
     const size_t smem = adapter_layout(NT, 128, a.stages_low, 0).bytes;
     const int e = ensure_smem(reinterpret_cast<const void*>(&k_adapter_low<NT>), smem);
     if (e != cudaSuccess) return e;
@@ -657,17 +804,18 @@ int launch_low(const CUtensorMap& map_a, const CUtensorMap& map_x, AdapterArgs a
 }
 
 template <int NT, typename OutT>
-int launch_proj(const CUtensorMap& map_w, const CUtensorMap& map_x, AdapterArgs a, cudaStream_t st)
+int launch_proj(const CUtensorMap& map_w, const CUtensorMap& map_x, const CUtensorMap& map_b, const CUtensorMap& map_s,
+                AdapterArgs a, cudaStream_t st)
 {
     const int rank = a.n_adapters > 0 ? a.rank : 0;
-    a.stages = stages_for(NT, a.rows, rank, NT == 256 ? 212 * 1024 : kProjBudget);
+    a.stages = stages_for(NT, a.rows, rank, NT > kSmallTile ? 212 * 1024 : kProjBudget);
     const size_t smem = adapter_layout(NT, a.rows, a.stages, rank).bytes;
     const void* f = reinterpret_cast<const void*>(&k_adapter_proj<NT, OutT>);
     const int e = ensure_smem(f, smem);
     if (e != cudaSuccess) return e;
     const int grid = persistent_grid(f, kGemmThreads, smem, static_cast<long long>(a.tiles) * a.mt);
     if (grid < 1) return cudaErrorLaunchOutOfResources;
-    return launch_kernel(&k_adapter_proj<NT, OutT>, dim3(grid), dim3(kGemmThreads), smem, st, 0, map_w, map_x, a);
+    return launch_kernel(&k_adapter_proj<NT, OutT>, dim3(grid), dim3(kGemmThreads), smem, st, 0, map_w, map_x, map_b, map_s, a);
 }
 
 }  // namespace
@@ -710,17 +858,23 @@ int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_
     }
 }
 
-int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const AdapterArgs& a,
-                        cudaStream_t st)
+int launch_adapter_split(int nt, const AdapterArgs& a, cudaStream_t st)
 {
-    auto go = [&](auto f, auto b) { return f32 ? f(map_w, map_x, a, st) : b(map_w, map_x, a, st); };
+    return nt == 128 ? launch_kernel(&k_adapter_split<128>, dim3(a.tiles, 8), dim3(256), 0, st, 0, a)
+                     : launch_kernel(&k_adapter_split<256>, dim3(a.tiles, 8), dim3(256), 0, st, 0, a);
+}
+
+int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const CUtensorMap& map_b,
+                        const CUtensorMap& map_s, const AdapterArgs& a, cudaStream_t st)
+{
     using B = __nv_bfloat16;
+    auto go = [&](auto f) { return f(map_w, map_x, map_b, map_s, a, st); };
     switch (nt) {
-        case 16: return go(&launch_proj<16, float>, &launch_proj<16, B>);
-        case 32: return go(&launch_proj<32, float>, &launch_proj<32, B>);
-        case 64: return go(&launch_proj<64, float>, &launch_proj<64, B>);
-        case 128: return go(&launch_proj<128, float>, &launch_proj<128, B>);
-        default: return go(&launch_proj<256, float>, &launch_proj<256, B>);
+        case 16: return f32 ? go(&launch_proj<16, float>) : go(&launch_proj<16, B>);
+        case 32: return f32 ? go(&launch_proj<32, float>) : go(&launch_proj<32, B>);
+        case 64: return f32 ? go(&launch_proj<64, float>) : go(&launch_proj<64, B>);
+        case 128: return go(&launch_proj<128, B>);
+        default: return go(&launch_proj<256, B>);
     }
 }
 

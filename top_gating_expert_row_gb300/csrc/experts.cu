@@ -284,7 +284,7 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     w.sort_bytes = moe_sort_workspace_bytes(p.T, p.topk, p.E, w.nt);
     if (route) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
     w.sort = part(o, w.sort_bytes);
-    w.h = part(o, std::max(cap, P) * p.I * 2);
+    w.h = part(o, std::max(cap, 2 * P) * p.I * 2);  // few pairs: fp32
     w.xs = part(o, w.nt >= kGatherColumns ? cap * p.H * 2 : 0);
     w.y = part(o, P * p.H * 4);
     w.bytes = o;
@@ -301,7 +301,7 @@ bool few_path(const mr_expert_params& p, const void* x, const void* w13, const v
 {
     const long long P = static_cast<long long>(p.T) * p.topk;
     return P <= kFewPairs && p.T <= kFewTokens && p.H % 8 == 0 && p.I % 8 == 0 && aligned(x, 16) && aligned(w13, 16) &&
-           aligned(w2, 16) && static_cast<size_t>(P) * p.I * 2 <= kFewSmem && static_cast<size_t>(p.T) * p.H * 2 <= kFewSmem;
+           aligned(w2, 16) && static_cast<size_t>(P) * p.I * 4 <= kFewSmem && static_cast<size_t>(p.T) * p.H * 2 <= kFewSmem;
 }
 
 FewArgs few_args(const mr_expert_params& p, const void* x, const void* w13, const void* w2, void* out, void* h)
@@ -310,7 +310,7 @@ FewArgs few_args(const mr_expert_params& p, const void* x, const void* w13, cons
     a.x = static_cast<const __nv_bfloat16*>(x);
     a.w13 = static_cast<const __nv_bfloat16*>(w13);
     a.w2 = static_cast<const __nv_bfloat16*>(w2);
-    a.h = static_cast<__nv_bfloat16*>(h);
+    a.h = static_cast<float*>(h);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.idx = nullptr;
     a.w = nullptr;
@@ -405,7 +405,7 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
 // Workspace of the adapter projection (the rank-space values; the plain kernels
 // use one slice) and its shapes.
 struct AdapterPlan {
-    size_t bytes;
+    size_t same, split, bytes;
     int nt, tiles, rows, mt, slices, groups;
     bool low_rows;
 };
@@ -420,11 +420,11 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
 {
     AdapterPlan w;
     // wide tiles of tokens read w less often; narrower ones while wide ones
-    // leave SMs without a unit
+    // leave SMs without a unit, and for fp32 outputs (k_adapter_proj says why)
     w.nt = 16;
     while (w.nt < 64 && w.nt < p.T) w.nt *= 2;
     const long long mt = (p.N + 127) / 128;
-    while (w.nt >= 64 && w.nt < 256 && (p.T + 2 * w.nt - 1) / (2 * w.nt) * mt >= kFullGrid) w.nt *= 2;
+    while (p.out_dtype == MR_BF16 && w.nt >= 64 && w.nt < 256 && (p.T + 2 * w.nt - 1) / (2 * w.nt) * mt >= kFullGrid) w.nt *= 2;
     w.tiles = (p.T + w.nt - 1) / w.nt;
     w.rows = rows_for(w.tiles, p.N, 1);
     w.mt = (p.N + w.rows - 1) / w.rows;
@@ -446,7 +446,11 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
         const int ksteps = (p.K + 63) / 64;
         w.slices = std::max(1, std::min(std::min(ksteps, 16), 128 / (w.tiles * w.groups)));
     }
-    w.bytes = static_cast<size_t>(w.slices) * p.T * p.rank * 4;
+    size_t o = 0;
+    part(o, static_cast<size_t>(w.slices) * p.T * p.rank * 4);
+    w.same = part(o, w.nt > 64 ? static_cast<size_t>(w.tiles) * 4 : 0);
+    w.split = part(o, w.nt > 64 ? static_cast<size_t>(p.T) * ((p.rank + 31) / 32) * 128 : 0);
+    w.bytes = o;
     return w;
 }
 
@@ -601,7 +605,7 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
     float* s = static_cast<float*>(workspace);
     const AdapterPlan plan = adapter_plan(*p);
     if (adapter_tensor_path(*p, plan, x, w, a, b)) {
-        CUtensorMap mapw, mapx, mapa;
+        CUtensorMap mapw, mapx, mapa, mapb, maps;
         const bool few = p->T <= kFewProjTokens && plan.low_rows && static_cast<size_t>(p->T) * p->K * 2 <= kFewSmem;
         if (!few && (!encode_map(&mapw, w, p->K, p->N, 0, plan.rows) || !encode_map(&mapx, x, p->K, p->T, 0, plan.nt)))
             return MR_ECUDA;
@@ -630,7 +634,18 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
             if (launch_adapter_low(plan.nt, mapa, mapx, d, plan.groups, st) != cudaSuccess) return MR_ECUDA;
         }
         if (few) return from_cuda(launch_adapter_few(x, w, p->out_dtype == MR_F32, d, st));
-        return from_cuda(launch_adapter_proj(plan.nt, p->out_dtype == MR_F32, mapw, mapx, d, st));
+        mapb = mapw;  // not read without adapters or by narrow tiles
+        maps = mapw;
+        if (p->n_adapters > 0 && plan.nt > 64) {
+            unsigned char* ws = static_cast<unsigned char*>(workspace);
+            d.same = reinterpret_cast<int32_t*>(ws + plan.same);
+            d.split = reinterpret_cast<B*>(ws + plan.split);
+            if (!encode_map(&mapb, b, p->rank, p->N, p->n_adapters, plan.rows) ||
+                !encode_map(&maps, d.split, (p->rank + 31) / 32 * 64, p->T, 0, plan.nt))
+                return MR_ECUDA;
+            if (launch_adapter_split(plan.nt, d, st) != cudaSuccess) return MR_ECUDA;
+        }
+        return from_cuda(launch_adapter_proj(plan.nt, p->out_dtype == MR_F32, mapw, mapx, mapb, maps, d, st));
     }
     const long long T = p->T;
     if (p->n_adapters > 0) {

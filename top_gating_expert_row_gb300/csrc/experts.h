@@ -60,6 +60,8 @@ struct AdapterArgs {
     const int32_t* adapter;    // [T]
     const float* scale;        // [n_adapters] or null
     float* low;                // [slices][T][rank] rank-space values, scaled
+    int32_t* same;             // wide tiles: the adapter of all the tile's tokens, or -1
+    __nv_bfloat16* split;      // wide tiles: [T][ranks / 32][hi of 32 ranks, lo of them]
     void* out;                 // [T][N]
     int32_t* status;           // timeouts
     int32_t* range_status;     // ids past the adapters (nullable)
@@ -75,8 +77,9 @@ int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_
                        cudaStream_t st);
 int launch_adapter_low_rows(const void* x, const void* wa, const AdapterArgs& a, cudaStream_t st);
 int launch_adapter_few(const void* x, const void* w, bool f32, const AdapterArgs& a, cudaStream_t st);
-int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const AdapterArgs& a,
-                        cudaStream_t st);
+int launch_adapter_split(int nt, const AdapterArgs& a, cudaStream_t st);
+int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const CUtensorMap& map_b,
+                        const CUtensorMap& map_s, const AdapterArgs& a, cudaStream_t st);
 
 // A tensor map of bf16 [planes][height][width] (planes 0: a matrix) with boxes
 // of box_h rows by 64 columns, 128-byte swizzled; elements outside read as 0.

@@ -25,7 +25,7 @@ struct FewArgs {
     const __nv_bfloat16* x;
     const __nv_bfloat16* w13;
     const __nv_bfloat16* w2;
-    __nv_bfloat16* h;       // [P][I]
+    float* h;               // [P][I]: few enough values to keep them unrounded
     __nv_bfloat16* out;
     const int32_t* idx;     // given choice (no routing)
     const float* w;
@@ -48,6 +48,20 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s)
         s = fmaf(__uint_as_float(p[i] & 0xffff0000u), __uint_as_float(q[i] & 0xffff0000u), s);
     }
     return s;
+}
+
+__device__ __forceinline__ float dot8(uint4 a, const float4* b, float s)
+{
+    const uint32_t p[4] = {a.x, a.y, a.z, a.w};
+    const float4 u = b[0], v = b[1];
+    s = fmaf(__uint_as_float(p[0] << 16), u.x, s);
+    s = fmaf(__uint_as_float(p[0] & 0xffff0000u), u.y, s);
+    s = fmaf(__uint_as_float(p[1] << 16), u.z, s);
+    s = fmaf(__uint_as_float(p[1] & 0xffff0000u), u.w, s);
+    s = fmaf(__uint_as_float(p[2] << 16), v.x, s);
+    s = fmaf(__uint_as_float(p[2] & 0xffff0000u), v.y, s);
+    s = fmaf(__uint_as_float(p[3] << 16), v.z, s);
+    return fmaf(__uint_as_float(p[3] & 0xffff0000u), v.w, s);
 }
 
 // Weights are read once: past L1.
@@ -94,7 +108,7 @@ __device__ __forceinline__ void few_up(const FewArgs& a, const int32_t* s_idx, c
         }
         sg = warp_sum(sg);
         sv = warp_sum(sv);
-        if (lane == 0) a.h[u] = __float2bfloat16_rn(act_f32(sg, a.act) * sv);
+        if (lane == 0) a.h[u] = act_f32(sg, a.act) * sv;
     }
 }
 
@@ -161,7 +175,7 @@ __device__ __forceinline__ void few_down(const FewArgs& a, const int32_t* s_idx,
             }
 #pragma unroll
             for (int k = 0; k < kChunks; ++k)
-                if (src[k] >= 0) sum = fmaf(weight[k], dot8(w[k], reinterpret_cast<const uint4*>(s_h)[src[k]], 0.0f), sum);
+                if (src[k] >= 0) sum = fmaf(weight[k], dot8(w[k], reinterpret_cast<const float4*>(s_h) + src[k] * 2, 0.0f), sum);
         }
         sum = warp_sum(sum);
         if (lane == 0) a.out[u] = __float2bfloat16_rn(sum);
@@ -197,7 +211,7 @@ __device__ __forceinline__ void few_body(const FewArgs& a, unsigned char* smem, 
         few_down_prefetch(a, s_idx);
         pdl_trigger();
         pdl_wait();
-        few_stage(s_v, a.h, P * a.I / 8);
+        few_stage(s_v, a.h, P * a.I / 4);
         __syncthreads();
         few_down(a, s_idx, s_w, s_v);
     }
@@ -205,7 +219,7 @@ __device__ __forceinline__ void few_body(const FewArgs& a, unsigned char* smem, 
 
 inline size_t few_smem(const FewArgs& a, bool down, size_t route_bytes)
 {
-    return few_pairs_bytes(a.T * a.topk) + static_cast<size_t>(align16(down ? a.T * a.topk * a.I * 2 : a.T * a.H * 2)) + route_bytes;
+    return few_pairs_bytes(a.T * a.topk) + static_cast<size_t>(align16(down ? a.T * a.topk * a.I * 4 : a.T * a.H * 2)) + route_bytes;
 }
 
 }  // namespace mr

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_layer_few(RouteArgs r, FewAr
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const WarpLayout L = warp_layout(r.k_r, r.stop, r.E, false, r.n_group > 0);
         unsigned char* wsm = smem + few_pairs_bytes(a.T * a.topk) +
-                             align16(DOWN ? a.T * a.topk * a.I * 2 : a.T * a.H * 2) + static_cast<size_t>(warp) * L.bytes;
+                             align16(DOWN ? a.T * a.topk * a.I * 4 : a.T * a.H * 2) + static_cast<size_t>(warp) * L.bytes;
         for (int t = warp; t < a.T; t += kFewWarps) {
             uint32_t warm = 0u;
             const float scale = route_row<MR_SCORE_FN, InT, NV, false, FULL>(r, t, wsm, L, lane, warm);
