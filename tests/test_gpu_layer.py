@@ -192,6 +192,9 @@ ADAPTERS = [
     (16, 256, 128, 32, 40, BF16), (48, 256, 512, 16, 64, BF16), (33, 72, 40, 24, 3, F32), (65, 128, 130, 16, 100, F32),
     (128, 320, 96, 128, 4, BF16), (200, 136, 264, 40, 7, F32), (600, 128, 256, 16, 3, BF16), (1100, 64, 128, 64, 900, F32),
     (300, 264, 200, 48, 2, F32), (5, 64, 64, 136, 2, F32),
+    # few units: the sum over K shared by clusters of 2, 4 and 8 CTAs
+    (8, 2048, 128, 16, 4, F32), (20, 1032, 256, 8, 3, BF16), (64, 4096, 2048, 16, 9, BF16), (40, 1544, 1000, 24, 40, F32),
+    (3, 4096, 64, 8, 2, F32), (4, 2056, 72, 40, 3, BF16),
     (1, 1, 1, 1, 1, F32), (5, 33, 17, 3, 4, F32), (9, 64, 31, 8, 2, BF16), (9, 64, 32, 5, 2, F32), (4, 30, 32, 8, 2, BF16),
 ]
 
@@ -215,6 +218,27 @@ def test_adapter_proj(mr, case):
     assert got.dtype == out
     assert_within(got, *adapter64(*v, out == BF16), "out")
     assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("T,K,r,n,segment", [
+    (20000, 64, 8, 7, 300), (20000, 64, 64, 5, 300), (20000, 72, 40, 3, 5000), (40000, 64, 128, 4, 700),
+    (40000, 128, 16, 40, 1), (40000, 64, 24, 3, 40000),
+])
+def test_adapter_wide_tiles(mr, T, K, r, n, segment):
+    """Prompts: tiles of 128 and 256 tokens that name one adapter, several, or none."""
+    N = 128
+    x, w, a, b, _, sc = make_adapters(T, K, N, r, n)
+    pick = torch.randint(-1, n, (-(-T // segment),), generator=_gen(8), dtype=torch.int32)
+    pick[0] = n - 1
+    ad = pick.repeat_interleave(segment)[:T].contiguous()
+    got = mr.adapter_proj(*[t.cuda() for t in (x, w, a, b, ad, sc)])
+    assert_within(got, *adapter64(x, w, a, b, ad, sc, True), "out")
+    if segment < T:  # the next request's adapter is corrupt: the others' tokens stay as they were
+        bad = int(ad[-1])
+        b[bad] = float("inf")
+        other = mr.adapter_proj(*[t.cuda() for t in (x, w, a, b, ad, sc)])
+        rest = (ad != bad).cuda() if bad >= 0 else torch.ones(T, dtype=torch.bool, device="cuda")
+        assert torch.equal(other[rest], got[rest])
 
 
 @pytest.mark.parametrize("T,K,N", [(1, 64, 64), (20, 128, 264), (300, 256, 128), (4, 33, 9)])

@@ -17,6 +17,9 @@
 //   b[i] with zeros, and an infinity in one request's adapter would reach every
 //   token of the tile.) In narrow tiles that is done before the sum over K is.
 //
+// Calls with fewer units than SMs share each unit's sum over K among the CTAs
+// of a cluster, which add their parts through distributed shared memory.
+//
 // k_adapter_proj starts while k_adapter_low runs (its sum over K needs nothing
 // of it), so the low-rank product costs little time of its own once w is large.
 #include <type_traits>
@@ -39,21 +42,18 @@ struct AdapterLayout {
 // rank: 0 for a kernel (or call) without the adapters' part. low: rank-space
 // values (small tiles: of all tokens; else of 16, rank-major); part: small
 // tiles: the adapters' part of the unit; else b[i]'s rows of the unit.
-__host__ __device__ inline AdapterLayout adapter_layout(int nt, int rows, int stages, int rank)
+__host__ __device__ inline AdapterLayout adapter_layout(int nt, int stages, int rank)
 {
     AdapterLayout L;
     uint32_t o = 0;
-    L.a = o; o += static_cast<uint32_t>(stages) * rows * kStepBytes;
+    L.a = o; o += static_cast<uint32_t>(stages) * kRows * kStepBytes;
     L.b = o; o += static_cast<uint32_t>(stages) * nt * kStepBytes;
-    // a product reads 128 rows from the start of a stage, also of the last one
-    const uint32_t reach = static_cast<uint32_t>(stages - 1) * rows * kStepBytes + 128 * kStepBytes;
-    if (o < reach) o = reach;
     L.ids = o; o += static_cast<uint32_t>(nt) * 4;
     L.list = o; o += static_cast<uint32_t>(nt) * 4 + 16;
     o = (o + 15) / 16 * 16;
     L.low = o; o += static_cast<uint32_t>(nt <= kSmallTile ? nt : 16) * rank * 4;
-    L.part = o; o += rank == 0 ? 0 : nt <= kSmallTile ? static_cast<uint32_t>(nt) * rows * 4
-                                                      : static_cast<uint32_t>(rows) * (rank + 8) * 2;
+    L.part = o; o += rank == 0 ? 0 : nt <= kSmallTile ? static_cast<uint32_t>(nt) * kRows * 4
+                                                      : static_cast<uint32_t>(kRows) * (rank + 8) * 2;
     o = (o + 15) / 16 * 16;
     L.bars = o; o += sizeof(GemmBars);
     L.bytes = o + 1024;
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const AdapterLayout L = adapter_layout(NT, 128, a.stages_low, 0);
+    const AdapterLayout L = adapter_layout(NT, a.stages_low, 0);
     GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
     int* slot = reinterpret_cast<int*>(smem + L.ids);    // token -> place in the list, -1: none
     int* list = reinterpret_cast<int*>(smem + L.list);   // the tile's distinct adapters, by first appearance
@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp == 1) {
         if (elect_one()) {
             int seen = 0;
+            StagePoll poll;
             const uint32_t desc = product_desc(cols);
             for (int g = blockIdx.z; ok && g < groups; g += gridDim.z, ++seen) {
                 const int buf = seen & 1;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 for (int k = k0; k < k1; ++k) {
-                    ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                    ok = poll.take(wait, bars, pos, a.stages_low);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t da = operand_desc(ring_a + pos.s * (128 * kStepBytes));
@@ -444,11 +445,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const AdapterLayout L = adapter_layout(NT, a.rows, a.stages, a.n_adapters > 0 ? a.rank : 0);
+    const AdapterLayout L = adapter_layout(NT, a.stages, a.n_adapters > 0 ? a.rank : 0);
     GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
     const int warp = threadIdx.x >> 5;
     constexpr uint32_t kColumns = 2 * NT;
-    const uint32_t a_bytes = a.rows * kStepBytes, b_bytes = NT * kStepBytes;
+    constexpr uint32_t a_bytes = kRows * kStepBytes, b_bytes = NT * kStepBytes;
     const uint32_t ring_a = smem_addr(smem + L.a), ring_b = smem_addr(smem + L.b);
 
     if (warp == 1) tmem_alloc(&bars.tmem, kColumns);
@@ -479,7 +480,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const Waits wait{&bars.gone, a.tries};
     const uint32_t drain = min(a.tries, kDrainTries);
     const int units = a.tiles * a.mt;
-    const int ksteps = (a.K + kStepK - 1) / kStepK;
+    // With fewer units than SMs a cluster of `ways` CTAs shares one, each a
+    // range of K (narrow tiles; one unit a cluster then).
+    const int ways = NT <= kSmallTile ? a.ways : 1, share = ways > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int first_unit = blockIdx.x / ways, stride = gridDim.x / ways;
+    const int all_steps = (a.K + kStepK - 1) / kStepK;
+    const int k_first = all_steps * share / ways, ksteps = all_steps * (share + 1) / ways - k_first;
     RingPos pos;
     int issued = 0;
     bool ok = true;
@@ -501,7 +507,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
     if (warp == 0 || warp == 2) {
         if (elect_one()) {
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            for (int u = first_unit; ok && u < units; u += stride) {
                 const int b = u / a.mt, m = u - b * a.mt;
                 int steps = ksteps, ad = early_adapter(b);
                 for (int k = 0; k < steps; ++k) {
@@ -513,11 +519,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (!a.drop) {
                         const uint32_t dst = warp == 0 ? ring_a + pos.s * a_bytes : ring_b + pos.s * b_bytes;
                         if (k < ksteps) {
-                            if (warp == 0) load_box2(dst, &map_w, k * kStepK, m * a.rows, full);
-                            else load_box2(dst, &map_x, k * kStepK, b * NT, full);
+                            if (warp == 0) load_box2(dst, &map_w, (k_first + k) * kStepK, m * kRows, full);
+                            else load_box2(dst, &map_x, (k_first + k) * kStepK, b * NT, full);
                         } else {
                             const int c = k - ksteps;
-                            if (warp == 0) load_box3(dst, &map_b, c * kChunkRanks, m * a.rows, ad, full);
+                            if (warp == 0) load_box3(dst, &map_b, c * kChunkRanks, m * kRows, ad, full);
                             else load_box2(dst, &map_s, c * kStepK, b * NT, full);
                         }
                     }
@@ -535,7 +541,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp == 1) {
         if (elect_one()) {
             int seen = 0;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            StagePoll poll;
+            for (int u = first_unit; ok && u < units; u += stride) {
                 const int b = u / a.mt;
                 const uint32_t desc = product_desc((min(NT, a.T - b * NT) + 15) & ~15);
                 const int early = early_adapter(b);
@@ -547,7 +554,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     tc_fence_after();
                     bool add = false;
                     for (int k = kSegments ? g * kSegment : 0; k < k1; ++k) {
-                        ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                        ok = poll.take(wait, bars, pos, a.stages);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t da = operand_desc(ring_a + pos.s * a_bytes), db = operand_desc(ring_b + pos.s * b_bytes);
@@ -561,7 +568,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                     if (ok && one_adapter(b, early) >= 0)
                         for (int c = 0; c < chunks; ++c) {
-                            ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                            ok = poll.take(wait, bars, pos, a.stages);
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t da = operand_desc(ring_a + pos.s * a_bytes), db = operand_desc(ring_b + pos.s * b_bytes);
@@ -587,13 +594,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         float* s = reinterpret_cast<float*>(smem + L.low);
         float* part = reinterpret_cast<float*>(smem + L.part);
         __nv_bfloat16* rows_b = reinterpret_cast<__nv_bfloat16*>(smem + L.part);
+        float* sums = reinterpret_cast<float*>(smem + L.a);    // shared unit: this CTA's sums, over the ring's first stages
         const int rank = a.rank, pitch = rank + 8;             // 16 bytes more a row: no bank conflicts
         if (low) pdl_wait();
         int seen = 0, tile = -1;
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        for (int u = first_unit; u < units; u += stride) {
             const int b = u / a.mt, m = u - b * a.mt, t0 = b * NT, tokens = min(NT, a.T - t0);
-            const int row = m * a.rows + et;
-            const bool there = et < a.rows && row < a.N;
+            const int row = m * kRows + et;
+            const bool there = row < a.N;
             if (low) {
                 epilogue_sync();  // the last unit's values have been read
                 if (b != tile)
@@ -609,18 +617,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             if (mine[t] >= 0) *reinterpret_cast<float4*>(s + t * rank + r) = low4(a, t0 + t, r);
                         }
                     epilogue_sync();
-                    const int er = et % a.rows, orow = m * a.rows + er;
-                    // this thread's row of the unit, every (128 / rows)-th token, 4 of them at a time
-                    const int every = kEpilogueThreads / a.rows;
-                    for (int tb = et / a.rows; tb < tokens; tb += 4 * every) {
+                    // this thread's row of the unit, 4 of this CTA's tokens at a time
+                    for (int tb = share; tb < tokens; tb += 4 * ways) {
                         float v[4] = {0, 0, 0, 0};
                         const __nv_bfloat16* brow[4];
                         bool use[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const int t = tb + k * every;
-                            use[k] = t < tokens && mine[t] >= 0 && orow < a.N;
-                            brow[k] = a.b + (use[k] ? (static_cast<long long>(mine[t]) * a.N + orow) * rank : 0);
+                            const int t = tb + k * ways;
+                            use[k] = t < tokens && mine[t] >= 0 && row < a.N;
+                            brow[k] = a.b + (use[k] ? (static_cast<long long>(mine[t]) * a.N + row) * rank : 0);
                         }
 #pragma unroll 2
                         for (int r = 0; r < rank; r += 8) {
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 if (!use[k]) continue;
                                 float w[8];
                                 unpack8(p[k], w);
-                                const float4* x = reinterpret_cast<const float4*>(s + (tb + k * every) * rank + r);
+                                const float4* x = reinterpret_cast<const float4*>(s + (tb + k * ways) * rank + r);
                                 const float4 y = x[0], z = x[1];
                                 v[k] = fmaf(w[0], y.x, fmaf(w[1], y.y, fmaf(w[2], y.z, fmaf(w[3], y.w, v[k]))));
                                 v[k] = fmaf(w[4], z.x, fmaf(w[5], z.y, fmaf(w[6], z.z, fmaf(w[7], z.w, v[k]))));
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            if (tb + k * every < tokens) part[(tb + k * every) * a.rows + er] = v[k];
+                            if (tb + k * ways < tokens) part[(tb + k * ways) * kRows + et] = v[k];
                     }
                 }
                 tile = b;
@@ -688,10 +694,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 16; ++c) v[c] += sum[kSegments ? c0 + c : 0];
                 }
+                if (ways > 1) {  // to the cluster, below
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) sums[(c0 + c) * kRows + et] = v[c];
+                    continue;
+                }
                 if (low && NT <= kSmallTile) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        if (et < a.rows && c0 + c < tokens) v[c] += part[(c0 + c) * a.rows + et];
+                        if (c0 + c < tokens) v[c] += part[(c0 + c) * kRows + et];
                 } else if (low && !summed) {
                     const int ad = mine[c0];
                     bool same = true, any = false;
@@ -711,11 +722,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             s[(r + 3) * 16 + c] = x.w;
                         }
                         if (same && ad != held) {
-                            for (int f = et; f < a.rows * (rank >> 3); f += kEpilogueThreads) {
+                            for (int f = et; f < kRows * (rank >> 3); f += kEpilogueThreads) {
                                 const int i = f / (rank >> 3), r = (f - i * (rank >> 3)) * 8;
-                                if (m * a.rows + i < a.N)
+                                if (m * kRows + i < a.N)
                                     *reinterpret_cast<uint4*>(rows_b + i * pitch + r) = __ldcg(reinterpret_cast<const uint4*>(
-                                        a.b + (static_cast<long long>(ad) * a.N + m * a.rows + i) * rank + r));
+                                        a.b + (static_cast<long long>(ad) * a.N + m * kRows + i) * rank + r));
                             }
                             held = ad;
                         }
@@ -770,6 +781,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_arrive(&bars.acc_empty[buf]);
         }
     }
+    if (ways > 1) {
+        // every CTA adds up its share of the tokens: the CTAs' sums in order of K
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 4 && !bars.gone && first_unit < units) {
+            const int et = threadIdx.x - kEpilogueThreads, b = first_unit / a.mt, m = first_unit - b * a.mt, t0 = b * NT;
+            const int tokens = min(NT, a.T - t0), row = m * kRows + et;
+            const float* part = reinterpret_cast<const float*>(smem + L.part);
+            const float* sums = reinterpret_cast<const float*>(smem + L.a) + et;
+            OutT* out = static_cast<OutT*>(a.out) + static_cast<long long>(t0) * a.N + row;
+            if (row < a.N)
+                for (int t = share; t < tokens; t += ways) {
+                    float v = 0.0f;
+#pragma unroll 8
+                    for (int r = 0; r < ways; ++r) v += *cluster_peer(sums + t * kRows, r);
+                    if (low) v += part[t * kRows + et];
+                    store_scalar(out + static_cast<long long>(t) * a.N, v);
+                }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while its sums may be read
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -785,18 +818,18 @@ namespace {
 // With narrow tiles k_adapter_proj leaves room for a CTA of k_adapter_low beside it.
 constexpr int kLowBudget = 60 * 1024, kProjBudget = 164 * 1024;
 
-int stages_for(int nt, int rows, int rank, int budget)
+int stages_for(int nt, int rank, int budget)
 {
     int s = kMaxStages;
-    while (s > 2 && static_cast<int>(adapter_layout(nt, rows, s, rank).bytes) > budget) --s;
+    while (s > 2 && static_cast<int>(adapter_layout(nt, s, rank).bytes) > budget) --s;
     return s;
 }
 
 template <int NT>
 int launch_low(const CUtensorMap& map_a, const CUtensorMap& map_x, AdapterArgs a, int groups, cudaStream_t st)
 {
-    a.stages_low = stages_for(NT, 128, 0, NT > kSmallTile ? kProjBudget : kLowBudget);
-    const size_t smem = adapter_layout(NT, 128, a.stages_low, 0).bytes;
+    a.stages_low = stages_for(NT, 0, NT > kSmallTile ? kProjBudget : kLowBudget);
+    const size_t smem = adapter_layout(NT, a.stages_low, 0).bytes;
     const int e = ensure_smem(reinterpret_cast<const void*>(&k_adapter_low<NT>), smem);
     if (e != cudaSuccess) return e;
     return launch_kernel(&k_adapter_low<NT>, dim3(a.tiles, a.slices, groups), dim3(kGemmThreads), smem, st, 0, map_a,
@@ -808,14 +841,16 @@ int launch_proj(const CUtensorMap& map_w, const CUtensorMap& map_x, const CUtens
                 AdapterArgs a, cudaStream_t st)
 {
     const int rank = a.n_adapters > 0 ? a.rank : 0;
-    a.stages = stages_for(NT, a.rows, rank, NT > kSmallTile ? 212 * 1024 : kProjBudget);
-    const size_t smem = adapter_layout(NT, a.rows, a.stages, rank).bytes;
+    a.stages = stages_for(NT, rank, NT > kSmallTile ? 212 * 1024 : kProjBudget);
+    const size_t smem = adapter_layout(NT, a.stages, rank).bytes;
     const void* f = reinterpret_cast<const void*>(&k_adapter_proj<NT, OutT>);
     const int e = ensure_smem(f, smem);
     if (e != cudaSuccess) return e;
-    const int grid = persistent_grid(f, kGemmThreads, smem, static_cast<long long>(a.tiles) * a.mt);
+    while (a.ways > 1 && !cluster_fits(f, kGemmThreads, smem, a.ways)) a.ways /= 2;
+    int grid = a.tiles * a.mt * a.ways;
+    if (a.ways == 1) grid = persistent_grid(f, kGemmThreads, smem, static_cast<long long>(a.tiles) * a.mt);
     if (grid < 1) return cudaErrorLaunchOutOfResources;
-    return launch_kernel(&k_adapter_proj<NT, OutT>, dim3(grid), dim3(kGemmThreads), smem, st, 0, map_w, map_x, map_b, map_s, a);
+    return launch_kernel(&k_adapter_proj<NT, OutT>, dim3(grid), dim3(kGemmThreads), smem, st, a.ways > 1 ? a.ways : 0, map_w, map_x, map_b, map_s, a);
 }
 
 }  // namespace

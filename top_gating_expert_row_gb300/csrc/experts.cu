@@ -227,7 +227,7 @@ int check_adapter(const mr_adapter_params* p)
 // use idx, w and h alone.
 struct ExpertPlan {
     size_t idx, w, h, xs, sids, eids, npp, y, sort, sort_bytes, bytes;
-    int nt, cap, rows_up, rows_down, mt_up, mt_down;
+    int nt, cap, mt_up, mt_down;
 };
 
 size_t part(size_t& o, size_t bytes)
@@ -252,14 +252,6 @@ int columns_for(long long P, int E)
     return nt;
 }
 
-// Weight rows of a stage: 128, fewer when that leaves SMs without a unit.
-int rows_for(long long blocks, int width, int per_row)
-{
-    int rows = 128;
-    while (rows > 32 && blocks * ((static_cast<long long>(width) * per_row + rows - 1) / rows) < kFullGrid) rows /= 2;
-    return rows;
-}
-
 // route: the routing options when the call routes too (room for its outputs and workspace)
 ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
 {
@@ -270,11 +262,8 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     while (w.nt > 16 && moe_sort_capacity(p.T, p.topk, p.E, w.nt) >= INT_MAX) w.nt /= 2;
     const size_t cap = moe_sort_capacity(p.T, p.topk, p.E, w.nt);
     w.cap = cap < INT_MAX ? static_cast<int>(cap) : -1;
-    const long long blocks = std::max<long long>(std::min<long long>(P, p.E), P / w.nt);
-    w.rows_up = rows_for(blocks, p.I, 2);
-    w.rows_down = rows_for(blocks, p.H, 1);
-    w.mt_up = (p.I + w.rows_up / 2 - 1) / (w.rows_up / 2);
-    w.mt_down = (p.H + w.rows_down - 1) / w.rows_down;
+    w.mt_up = (p.I + 63) / 64;
+    w.mt_down = (p.H + 127) / 128;
     size_t o = 0;
     w.idx = part(o, route ? P * 4 : 0);
     w.w = part(o, route ? P * 4 : 0);
@@ -365,7 +354,7 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     const int box = token_box(plan.nt);
     if (!encode_map(&map13, w13, p.H, 2ll * p.I, p.E, 16) ||
         !encode_map(&mapx, gather ? ws + plan.xs : x, p.H, gather ? plan.cap : p.T, 0, gather ? box : 1) ||
-        !encode_map(&map2, w2, p.I, p.H, p.E, plan.rows_down) || !encode_map(&maph, ws + plan.h, p.I, plan.cap, 0, box))
+        !encode_map(&map2, w2, p.I, p.H, p.E, 128) || !encode_map(&maph, ws + plan.h, p.I, plan.cap, 0, box))
         return MR_ECUDA;
     ExpertArgs a;
     a.x = static_cast<const __nv_bfloat16*>(x);
@@ -390,13 +379,11 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     a.act = p.act;
     wait_test(&a.tries, &a.drop);
     const long long blocks = plan.cap / plan.nt;
-    a.rows = plan.rows_up;
     a.mt = plan.mt_up;
     int e = gather ? launch_experts_gather(a, st) : cudaSuccess;
     if (e != cudaSuccess) return MR_ECUDA;
     e = launch_experts_up(plan.nt, map13, mapx, a, blocks * a.mt, st);
     if (e != cudaSuccess) return MR_ECUDA;
-    a.rows = plan.rows_down;
     a.mt = plan.mt_down;
     e = launch_experts_down(plan.nt, map2, maph, a, blocks * a.mt, st);
     return e != cudaSuccess ? MR_ECUDA : from_cuda(launch_experts_sum(a, st));
@@ -406,7 +393,7 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
 // use one slice) and its shapes.
 struct AdapterPlan {
     size_t same, split, bytes;
-    int nt, tiles, rows, mt, slices, groups;
+    int nt, tiles, mt, ways, slices, groups;
     bool low_rows;
 };
 
@@ -426,8 +413,11 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
     const long long mt = (p.N + 127) / 128;
     while (p.out_dtype == MR_BF16 && w.nt >= 64 && w.nt < 256 && (p.T + 2 * w.nt - 1) / (2 * w.nt) * mt >= kFullGrid) w.nt *= 2;
     w.tiles = (p.T + w.nt - 1) / w.nt;
-    w.rows = rows_for(w.tiles, p.N, 1);
-    w.mt = (p.N + w.rows - 1) / w.rows;
+    w.mt = static_cast<int>(mt);
+    // a cluster shares a unit's sum over K while that gives idle SMs work
+    const int steps = (p.K + 63) / 64;
+    w.ways = 1;
+    while (w.nt <= 64 && w.ways < 8 && 2ll * w.ways * w.tiles * w.mt <= kFullGrid && steps / (2 * w.ways) >= 4) w.ways *= 2;
     w.slices = 1;
     w.groups = 1;
     w.bytes = 0;
@@ -438,13 +428,14 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
         const long long warps = static_cast<long long>(p.T) * ((p.rank + 3) / 4);
         while (w.slices < 8 && warps * w.slices < 1024 && p.K / (w.slices * 2) >= 512) w.slices *= 2;
     } else if (p.rank <= 128) {
-        // as many CTAs as SMs or a little fewer: groups of adapters first (as
-        // many as the tile's tokens can name), then slices of K
-        const int distinct = std::min(std::min(w.nt, p.T), p.n_adapters);
-        const int per_group = std::max(1, 128 / p.rank);
-        w.groups = std::min((distinct + per_group - 1) / per_group, std::max(1, 128 / w.tiles));
+        // as many CTAs as SMs or a little fewer: slices of K first (a prompt's
+        // tile names one adapter), then groups of as many adapters as a tile's
+        // tokens can name
         const int ksteps = (p.K + 63) / 64;
-        w.slices = std::max(1, std::min(std::min(ksteps, 16), 128 / (w.tiles * w.groups)));
+        w.slices = std::max(1, std::min(std::min(ksteps, 16), 144 / w.tiles));
+        const int distinct = std::min(std::min(w.nt, p.T), p.n_adapters);
+        const int per_group = 128 / p.rank;
+        w.groups = std::max(1, std::min((distinct + per_group - 1) / per_group, 144 / (w.tiles * w.slices)));
     }
     size_t o = 0;
     part(o, static_cast<size_t>(w.slices) * p.T * p.rank * 4);
@@ -607,7 +598,7 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
     if (adapter_tensor_path(*p, plan, x, w, a, b)) {
         CUtensorMap mapw, mapx, mapa, mapb, maps;
         const bool few = p->T <= kFewProjTokens && plan.low_rows && static_cast<size_t>(p->T) * p->K * 2 <= kFewSmem;
-        if (!few && (!encode_map(&mapw, w, p->K, p->N, 0, plan.rows) || !encode_map(&mapx, x, p->K, p->T, 0, plan.nt)))
+        if (!few && (!encode_map(&mapw, w, p->K, p->N, 0, 128) || !encode_map(&mapx, x, p->K, p->T, 0, plan.nt)))
             return MR_ECUDA;
         AdapterArgs d;
         d.b = static_cast<const B*>(b);
@@ -623,8 +614,8 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
         d.n_adapters = p->n_adapters;
         d.rank = p->rank;
         d.tiles = plan.tiles;
-        d.rows = plan.rows;
         d.mt = plan.mt;
+        d.ways = plan.ways;
         d.slices = plan.slices;
         wait_test(&d.tries, &d.drop);
         if (p->n_adapters > 0 && plan.low_rows) {
@@ -640,7 +631,7 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
             unsigned char* ws = static_cast<unsigned char*>(workspace);
             d.same = reinterpret_cast<int32_t*>(ws + plan.same);
             d.split = reinterpret_cast<B*>(ws + plan.split);
-            if (!encode_map(&mapb, b, p->rank, p->N, p->n_adapters, plan.rows) ||
+            if (!encode_map(&mapb, b, p->rank, p->N, p->n_adapters, 128) ||
                 !encode_map(&maps, d.split, (p->rank + 31) / 32 * 64, p->T, 0, plan.nt))
                 return MR_ECUDA;
             if (launch_adapter_split(plan.nt, d, st) != cudaSuccess) return MR_ECUDA;

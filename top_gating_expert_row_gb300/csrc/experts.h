@@ -35,7 +35,6 @@ struct ExpertArgs {
     __nv_bfloat16* out;    // [T][H]
     int32_t* status;
     int T, topk, H, I, E, P, cap;
-    int rows;              // weight rows of a stage (up: gate and up rows together)
     int mt;                // row tiles of this kernel
     int stages, act, drop;
     int out16;             // out allows 16-byte stores
@@ -67,7 +66,8 @@ struct AdapterArgs {
     int32_t* range_status;     // ids past the adapters (nullable)
     int T, K, N, n_adapters, rank;
     int tiles;                 // of at most nt tokens
-    int rows, mt;              // weight rows of a stage, row tiles
+    int mt;                    // row tiles
+    int ways;                  // CTAs (a cluster) that share the sum over K of a unit
     int slices;                // of K, in k_adapter_low
     int stages, stages_low, drop;
     uint32_t tries;

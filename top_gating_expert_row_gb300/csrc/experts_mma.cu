@@ -6,8 +6,8 @@
 //   k_experts_sum   out[t] = sum_j y[t][j], in slot order
 //
 // The first two are one persistent CTA per SM over units (block, row tile); see gemm.cuh
-// for the operands' roles. A unit of `up` holds rows/2 gate rows and the same
-// rows/2 up rows, alternating by 16, so that a warp of the epilogue has both
+// for the operands' roles. A unit of `up` holds 64 gate rows and the same 64 up
+// rows, alternating by 16, so that a warp of the epilogue has both
 // factors of h and one shuffle brings them together.
 //
 // Blocks of 64 pairs and more (prompts) read x from a copy in sorted order that
@@ -34,15 +34,12 @@ struct CtaLayout {
 };
 
 // Offsets from the first 1024-byte boundary of the CTA's shared memory.
-__host__ __device__ inline CtaLayout cta_layout(int nt, int rows, int stages)
+__host__ __device__ inline CtaLayout cta_layout(int nt, int stages)
 {
     CtaLayout L;
     uint32_t o = 0;
-    L.a = o; o += static_cast<uint32_t>(stages) * rows * kStepBytes;
+    L.a = o; o += static_cast<uint32_t>(stages) * kRows * kStepBytes;
     L.b = o; o += static_cast<uint32_t>(stages) * nt * kStepBytes;
-    // a product reads 128 rows from the start of a stage, also of the last one
-    const uint32_t reach = static_cast<uint32_t>(stages - 1) * rows * kStepBytes + 128 * kStepBytes;
-    if (o < reach) o = reach;
     L.info = o; o += static_cast<uint32_t>(nt) * 8;
     o = (o + 15) / 16 * 16;
     L.bars = o; o += sizeof(GemmBars);
@@ -128,11 +125,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const CtaLayout L = cta_layout(NT, a.rows, a.stages);
+    const CtaLayout L = cta_layout(NT, a.stages);
     GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr uint32_t kColumns = 2 * NT;  // two accumulators: one fills while the other is read
-    const uint32_t a_bytes = a.rows * kStepBytes, b_bytes = NT * kStepBytes;
+    constexpr uint32_t a_bytes = kRows * kStepBytes, b_bytes = NT * kStepBytes;
     const uint32_t ring_a = smem_addr(smem + L.a), ring_b = smem_addr(smem + L.b);
 
     if (warp == 1) tmem_alloc(&bars.tmem, kColumns);
@@ -184,10 +181,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     ++issued;
                     if (!a.drop) {
                         if (DOWN) {
-                            load_box3(dst, &map_w, k * kStepK, m * a.rows, e, full);
+                            load_box3(dst, &map_w, k * kStepK, m * kRows, e, full);
                         } else {
-                            const int i = m * (a.rows >> 1);
-                            for (int g = 0; g < a.rows >> 5; ++g) {
+                            const int i = m * (kRows / 2);
+                            for (int g = 0; g < kRows / 32; ++g) {
                                 load_box3(dst + g * 32 * kStepBytes, &map_w, k * kStepK, i + g * 16, e, full);
                                 load_box3(dst + (g * 32 + 16) * kStepBytes, &map_w, k * kStepK, a.I + i + g * 16, e, full);
                             }
@@ -252,6 +249,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if (DOWN) pdl_wait();
             int seen = 0;
             bool ok = true;
+            StagePoll poll;
             for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++seen) {
                 const int buf = seen & 1;
                 ok = seen < 2 || wait(&bars.acc_empty[buf], ((seen >> 1) - 1) & 1);
@@ -260,7 +258,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const uint32_t d = tmem + buf * NT;
                 uint32_t desc = 0;
                 for (int k = 0; k < ksteps; ++k) {
-                    ok = wait(&bars.full[pos.s], pos.wraps & 1);
+                    ok = poll.take(wait, bars, pos, a.stages);
                     if (!ok) break;
                     tc_fence_after();
                     if (k == 0) desc = product_desc(bars.cols[pos.s]);
@@ -298,8 +296,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             tc_fence_after();
             const uint32_t acc = tmem + buf * NT + (static_cast<uint32_t>(q * 32) << 16);
             if (DOWN) {
-                const int row = m * a.rows + et;
-                const bool mine = et < a.rows && row < a.H;
+                const int row = m * kRows + et;
+                const bool mine = row < a.H;
                 for (int c0 = 0; c0 < n; c0 += 16) {
                     float v[16];
                     tmem_load16(acc + c0, v);
@@ -315,11 +313,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 // lanes 0-15 hold gate rows, lanes 16-31 the same up rows: the
                 // first finish the even columns, the others the odd ones
                 const bool low = lane < 16;
-                const int col = m * (a.rows >> 1) + q * 16 + (lane & 15);
-                const bool mine = q * 32 < a.rows && col < a.I;
+                const int col = m * (kRows / 2) + q * 16 + (lane & 15);
+                const bool mine = col < a.I;
                 __nv_bfloat16* h = a.h + (static_cast<long long>(b) * NT + (low ? 0 : 1)) * a.I + col;
-                if (q * 32 < a.rows)
-                    for (int c0 = 0; c0 < n; c0 += 16) {
+                for (int c0 = 0; c0 < n; c0 += 16) {
                         float v[16];
                         tmem_load16(acc + c0, v);
 #pragma unroll
@@ -365,19 +362,18 @@ namespace {
 constexpr int kSmemBudget = 200 * 1024;
 
 // As many stages as the budget holds.
-int stages_for(int nt, int rows, int ksteps)
+int stages_for(int nt)
 {
     int s = kMaxStages;
-    while (s > 2 && cta_layout(nt, rows, s).bytes > kSmemBudget) --s;
-    (void)ksteps;
+    while (s > 2 && cta_layout(nt, s).bytes > kSmemBudget) --s;
     return s;
 }
 
 template <int NT, bool DOWN>
 int launch_one(const CUtensorMap& map_w, const CUtensorMap& map_t, ExpertArgs a, long long units, cudaStream_t st)
 {
-    a.stages = stages_for(NT, a.rows, 0);
-    const size_t smem = cta_layout(NT, a.rows, a.stages).bytes;
+    a.stages = stages_for(NT);
+    const size_t smem = cta_layout(NT, a.stages).bytes;
     const void* f = reinterpret_cast<const void*>(&k_experts<NT, DOWN>);
     const int e = ensure_smem(f, smem);
     if (e != cudaSuccess) return e;
