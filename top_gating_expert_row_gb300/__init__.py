@@ -510,14 +510,15 @@ def aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor, T: in
 
 
 def _check(what: str, t: torch.Tensor, shape, dtype, device) -> None:
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, x on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    raise ValueError(f"{what} must be contiguous")
 
 
 def _check_status(status, device) -> Optional[int]:
@@ -537,8 +538,6 @@ class _Launch:
     __slots__ = ("index", "device", "stream")
 
     def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError(f"x must be on a CUDA device, got {device}")
         self.index, self.device, self.stream = device.index, None, None
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
@@ -546,7 +545,7 @@ class _Launch:
             if stream.device != device:
                 raise ValueError(f"stream is on {stream.device}, x on {device}")
             self.stream = torch.cuda.stream(stream)
-        elif self.index != torch.cuda.current_device():
+        else:
             self.device = torch.cuda.device(device)
 
     def __enter__(self):
@@ -561,6 +560,29 @@ class _Launch:
             self.stream.__exit__(*exc)
         if self.device is not None:
             self.device.__exit__(*exc)
+
+
+class _Here:
+    """_Launch where the device is current already and the stream its current one."""
+
+    __slots__ = ("raw",)
+
+    def __init__(self, index):
+        self.raw = torch._C._cuda_getCurrentRawStream(index)
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *exc):
+        pass
+
+
+def _launch(device, stream):
+    if device.type != "cuda":
+        raise ValueError(f"x must be on a CUDA device, got {device}")
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return _Here(device.index)
+    return _Launch(device, stream)
 
 
 # The options of a call and the workspace it needs depend on its sizes alone: kept, so that a decode step does not
@@ -609,7 +631,7 @@ def experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, w13: 
     _check("topk_w", topk_w, (T, k), torch.float32, dev)
     st = _check_status(status, dev)
     p, nb = _experts_plan(T, H, I, E, k, act)
-    with _Launch(dev, stream) as raw:
+    with _launch(dev, stream) as raw:
         out = torch.empty_like(x)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev)
         _ok(_lib.moe_experts_fwd(p, x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), w13.data_ptr(),
@@ -636,7 +658,7 @@ def layer(x: torch.Tensor, logits: torch.Tensor, topk: int, w13: torch.Tensor, w
         _check("bias", bias, (E,), torch.float32, dev)
         cp = mr_router_params(*options, bias.data_ptr())
         p, nb = ctypes.byref(cp), moe_layer_workspace_bytes(cp, H, I, act)
-    with _Launch(dev, stream) as raw:
+    with _launch(dev, stream) as raw:
         out = torch.empty_like(x)
         idx = torch.empty(T, max(topk, 0), dtype=torch.int32, device=dev)
         w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=dev)
@@ -678,7 +700,7 @@ def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = N
             _check("scale", scale, (n,), torch.float32, dev)
             ps = scale.data_ptr()
     p, nb = _adapter_plan(T, K, N, n, rank, out_dtype == torch.float32)
-    with _Launch(dev, stream) as raw:
+    with _launch(dev, stream) as raw:
         out = torch.empty(T, N, dtype=out_dtype, device=dev)
         ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
         _ok(_lib.moe_adapter_proj_fwd(p, x.data_ptr(), w.data_ptr(), pa, pb, pi, ps, out.data_ptr(),

@@ -294,30 +294,57 @@ __global__ void __launch_bounds__(256) k_adapter_low_rows(const __nv_bfloat16* x
 }
 
 // One to TOKENS tokens: a warp per row of w, on the CUDA cores (few.cuh says
-// why). The row's product, and the loads of b's row, come before the wait for
-// the rank-space values; the lanes share out the ranks.
-template <int TOKENS, typename OutT>
-__global__ void __launch_bounds__(256) k_adapter_few(const __nv_bfloat16* x, const __nv_bfloat16* w, AdapterArgs a)
+// why). The row's product, and the loads of b's row, come before the rank-space
+// values are needed; the lanes share out the ranks. FUSED (one token): every CTA
+// makes the rank-space values itself, at most 64 KB of a from L2: a launch less
+// for the host, which costs an eager call 4.5 us, and up to 1.2 us more on the
+// GPU (5.0 against 3.8 at K=2048 N=256, 5.6 against 5.9 at K=N=2048).
+__host__ __device__ constexpr int few_threads(bool fused) { return fused ? 512 : 256; }
+
+template <int TOKENS, bool FUSED, typename OutT>
+__global__ void __launch_bounds__(few_threads(FUSED)) k_adapter_few(const __nv_bfloat16* x, const __nv_bfloat16* w,
+                                                     const __nv_bfloat16* wa, AdapterArgs a)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     const bool low = a.n_adapters > 0;
-    if (!low) pdl_wait();
+    if (!low || FUSED) pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, K8 = a.K / 8;
-    for (int i = threadIdx.x; i < a.T * K8; i += 256)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, K8 = a.K / 8;
+    const uint4* xs = reinterpret_cast<const uint4*>(smem);
+    float* s_low = reinterpret_cast<float*>(smem + static_cast<size_t>(a.T) * a.K * 2);
+    constexpr int kChunks = 8, kThreads = few_threads(FUSED), kWarps = kThreads / 32;
+    bool waited = !low || FUSED;
+    // the first part of the warp's first row is on its way while x is staged
+    int row = blockIdx.x * kWarps + warp;
+    uint4 wc[kChunks];
+    auto load = [&](int c0) {
+        const uint4* wr = reinterpret_cast<const uint4*>(w + static_cast<long long>(row) * a.K);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+            if (c0 + c * 32 < K8) wc[c] = load_weights(wr + c0 + c * 32);
+    };
+    if (row < a.N) load(lane);
+    for (int i = threadIdx.x; i < a.T * K8; i += kThreads)
         reinterpret_cast<uint4*>(smem)[i] = __ldcg(reinterpret_cast<const uint4*>(x) + i);
     __syncthreads();
-    const uint4* xs = reinterpret_cast<const uint4*>(smem);
-    constexpr int kChunks = 8;
-    bool waited = !low;
-    for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < a.N; row += gridDim.x * 8) {
-        const uint4* wr = reinterpret_cast<const uint4*>(w + static_cast<long long>(row) * a.K);
+    if (FUSED && low) {
+        for (int u = warp; u < a.T * a.rank; u += kWarps) {
+            const int t = u / a.rank, r = u - t * a.rank, id = __ldcg(a.adapter + t);
+            if (id >= a.n_adapters && r == 0 && lane == 0 && blockIdx.x == 0) report_status(a.range_status, kStatusRange);
+            if (id < 0 || id >= a.n_adapters) continue;
+            const uint4* ar = reinterpret_cast<const uint4*>(wa + (static_cast<long long>(id) * a.rank + r) * a.K);
+            float v = 0.0f;
+#pragma unroll 8
+            for (int c = lane; c < K8; c += 32) v = dot8(__ldcg(ar + c), xs[t * K8 + c], v);
+            v = warp_sum(v);
+            if (lane == 0) s_low[u] = a.scale ? v * __ldcg(a.scale + id) : v;
+        }
+        __syncthreads();
+    }
+    for (; row < a.N; row += gridDim.x * kWarps) {
         float sum[TOKENS] = {};
         for (int c0 = lane; c0 < K8; c0 += 32 * kChunks) {
-            uint4 wc[kChunks];
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                if (c0 + c * 32 < K8) wc[c] = load_weights(wr + c0 + c * 32);
+            if (c0 != lane || row != static_cast<int>(blockIdx.x) * kWarps + warp) load(c0);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
                 if (c0 + c * 32 < K8) {
@@ -346,7 +373,9 @@ __global__ void __launch_bounds__(256) k_adapter_few(const __nv_bfloat16* x, con
                 const float* s = a.low + static_cast<long long>(t) * a.rank;
                 for (int r = lane; r < a.rank; r += 32) {
                     float v = 0.0f;
-                    for (int p = 0; p < a.slices; ++p) v += __ldcg(s + static_cast<long long>(p) * a.T * a.rank + r);
+                    if (FUSED) v = s_low[t * a.rank + r];
+                    else
+                        for (int p = 0; p < a.slices; ++p) v += __ldcg(s + static_cast<long long>(p) * a.T * a.rank + r);
                     sum[t] = fmaf(r == lane ? b0[t] : load_scalar(br + r), v, sum[t]);
                 }
             }
@@ -596,7 +625,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         __nv_bfloat16* rows_b = reinterpret_cast<__nv_bfloat16*>(smem + L.part);
         float* sums = reinterpret_cast<float*>(smem + L.a);    // shared unit: this CTA's sums, over the ring's first stages
         const int rank = a.rank, pitch = rank + 8;             // 16 bytes more a row: no bank conflicts
-        if (low) pdl_wait();
+        if (low && NT <= kSmallTile && first_unit < units) {
+            // b's rows of the first unit come to L2 while the rank-space values are made
+            const int b = first_unit / a.mt, m = first_unit - b * a.mt, t = b * NT + share + et * ways;
+            const int id = et * ways + share < NT && t < a.T ? __ldcg(a.adapter + t) : -1;
+            if (id >= 0 && id < a.n_adapters)
+                prefetch_l2(a.b + (static_cast<long long>(id) * a.N + m * kRows) * rank, min(kRows, a.N - m * kRows) * rank * 2);
+        }
         int seen = 0, tile = -1;
         for (int u = first_unit; u < units; u += stride) {
             const int b = u / a.mt, m = u - b * a.mt, t0 = b * NT, tokens = min(NT, a.T - t0);
@@ -609,33 +644,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         const int id = t < tokens ? __ldcg(a.adapter + t0 + t) : -1;
                         mine[t] = id < a.n_adapters ? max(id, -1) : -1;
                     }
+                if (NT <= kSmallTile) epilogue_sync();
+                if (!waited) pdl_wait();  // for the rank-space values
+                waited = true;
                 if (NT <= kSmallTile) {
-                    epilogue_sync();
                     if (b != tile)
-                        for (int f = et; f < tokens * (rank >> 2); f += kEpilogueThreads) {
-                            const int t = f / (rank >> 2), r = (f - t * (rank >> 2)) * 4;
+                        for (int f = et; share + f / (rank >> 2) * ways < tokens; f += kEpilogueThreads) {
+                            const int t = share + f / (rank >> 2) * ways, r = f % (rank >> 2) * 4;
                             if (mine[t] >= 0) *reinterpret_cast<float4*>(s + t * rank + r) = low4(a, t0 + t, r);
                         }
                     epilogue_sync();
-                    // this thread's row of the unit, 4 of this CTA's tokens at a time
-                    for (int tb = share; tb < tokens; tb += 4 * ways) {
-                        float v[4] = {0, 0, 0, 0};
-                        const __nv_bfloat16* brow[4];
-                        bool use[4];
+                    // this thread's row of the unit, 8 of this CTA's tokens at a time
+                    for (int tb = share; tb < tokens; tb += 8 * ways) {
+                        float v[8] = {};
+                        const __nv_bfloat16* brow[8];
+                        bool use[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 8; ++k) {
                             const int t = tb + k * ways;
                             use[k] = t < tokens && mine[t] >= 0 && row < a.N;
                             brow[k] = a.b + (use[k] ? (static_cast<long long>(mine[t]) * a.N + row) * rank : 0);
                         }
 #pragma unroll 2
                         for (int r = 0; r < rank; r += 8) {
-                            uint4 p[4];
+                            uint4 p[8];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
+                            for (int k = 0; k < 8; ++k)
                                 if (use[k]) p[k] = __ldcg(reinterpret_cast<const uint4*>(brow[k] + r));
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < 8; ++k) {
                                 if (!use[k]) continue;
                                 float w[8];
                                 unpack8(p[k], w);
@@ -646,7 +683,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             }
                         }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < 8; ++k)
                             if (tb + k * ways < tokens) part[(tb + k * ways) * kRows + et] = v[k];
                     }
                 }
@@ -791,13 +828,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const float* part = reinterpret_cast<const float*>(smem + L.part);
             const float* sums = reinterpret_cast<const float*>(smem + L.a) + et;
             OutT* out = static_cast<OutT*>(a.out) + static_cast<long long>(t0) * a.N + row;
+            constexpr int kAtOnce = 4;  // tokens whose parts are in flight together
             if (row < a.N)
-                for (int t = share; t < tokens; t += ways) {
-                    float v = 0.0f;
-#pragma unroll 8
-                    for (int r = 0; r < ways; ++r) v += *cluster_peer(sums + t * kRows, r);
-                    if (low) v += part[t * kRows + et];
-                    store_scalar(out + static_cast<long long>(t) * a.N, v);
+                for (int t = share; t < tokens; t += kAtOnce * ways) {
+                    float p[kAtOnce][8];
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            p[k][r] = r < ways && t + k * ways < tokens ? *cluster_peer(sums + (t + k * ways) * kRows, r) : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        if (t + k * ways >= tokens) break;
+                        float v = p[k][0];
+#pragma unroll
+                        for (int r = 1; r < 8; ++r) v += p[k][r];
+                        if (low) v += part[(t + k * ways) * kRows + et];
+                        store_scalar(out + static_cast<long long>(t + k * ways) * a.N, v);
+                    }
                 }
         }
         __syncwarp();
@@ -864,21 +912,25 @@ int launch_adapter_low_rows(const void* x, const void* wa, const AdapterArgs& a,
                          static_cast<const __nv_bfloat16*>(wa), a);
 }
 
-int launch_adapter_few(const void* x, const void* w, bool f32, const AdapterArgs& a, cudaStream_t st)
+int launch_adapter_few(const void* x, const void* w, const void* wa, bool fused, bool f32, const AdapterArgs& a,
+                       cudaStream_t st)
 {
     using B = __nv_bfloat16;
-    const size_t smem = static_cast<size_t>(a.T) * a.K * 2;
+    const size_t smem = static_cast<size_t>(a.T) * a.K * 2 + (fused && a.n_adapters > 0 ? static_cast<size_t>(a.T) * a.rank * 4 : 0);
     auto go = [&](auto kernel) -> int {
         const void* f = reinterpret_cast<const void*>(kernel);
         const int e = ensure_smem(f, smem);
         if (e != cudaSuccess) return e;
-        const int grid = persistent_grid(f, 256, smem, (a.N + 7) / 8);
+        const int threads = few_threads(fused), grid = persistent_grid(f, threads, smem, (a.N + threads / 32 - 1) / (threads / 32));
         if (grid < 1) return cudaErrorLaunchOutOfResources;
-        return launch_kernel(kernel, dim3(grid), dim3(256), smem, st, 0, static_cast<const B*>(x), static_cast<const B*>(w), a);
+        return launch_kernel(kernel, dim3(grid), dim3(threads), smem, st, 0, static_cast<const B*>(x), static_cast<const B*>(w),
+                             static_cast<const B*>(wa), a);
     };
-    if (a.T == 1) return f32 ? go(&k_adapter_few<1, float>) : go(&k_adapter_few<1, B>);
-    if (a.T == 2) return f32 ? go(&k_adapter_few<2, float>) : go(&k_adapter_few<2, B>);
-    return f32 ? go(&k_adapter_few<4, float>) : go(&k_adapter_few<4, B>);
+    auto out = [&](auto as_f32, auto as_bf16) { return f32 ? go(as_f32) : go(as_bf16); };
+    if (fused) return out(&k_adapter_few<1, true, float>, &k_adapter_few<1, true, B>);
+    if (a.T == 1) return out(&k_adapter_few<1, false, float>, &k_adapter_few<1, false, B>);
+    if (a.T == 2) return out(&k_adapter_few<2, false, float>, &k_adapter_few<2, false, B>);
+    return out(&k_adapter_few<4, false, float>, &k_adapter_few<4, false, B>);
 }
 
 int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_x, const AdapterArgs& a, int groups,

@@ -400,8 +400,13 @@ struct AdapterPlan {
 // Rank-space values: up to this many products a warp per four of them, above
 // it the tensor cores.
 constexpr long long kLowRowsProducts = 64ll << 20;
-// Tokens that the projection on the CUDA cores takes, and their shared memory.
+// What the projection on the CUDA cores takes: up to 4 tokens, and products up
+// to T*N*K = 10M (T=1 K=4096: 7.0 us against 7.7 on the tensor cores at N=2048,
+// 11.5 against 8.6 at N=4096; T=2 K=N=2048: 6.7 against 7.5).
 constexpr int kFewProjTokens = 4;
+constexpr long long kFewProjProducts = 10000000;
+// Rank-space values that every CTA of it makes for itself (one token), up to this many products.
+constexpr long long kFusedLowProducts = 32 << 10;
 
 AdapterPlan adapter_plan(const mr_adapter_params& p)
 {
@@ -415,9 +420,12 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
     w.tiles = (p.T + w.nt - 1) / w.nt;
     w.mt = static_cast<int>(mt);
     // a cluster shares a unit's sum over K while that gives idle SMs work
+    // (clusters of 8 fit the GPU's partitions badly when there are many)
     const int steps = (p.K + 63) / 64;
     w.ways = 1;
-    while (w.nt <= 64 && w.ways < 8 && 2ll * w.ways * w.tiles * w.mt <= kFullGrid && steps / (2 * w.ways) >= 4) w.ways *= 2;
+    while (w.nt <= 64 && w.ways < 8 && 2ll * w.ways * w.tiles * w.mt <= kFullGrid && steps / (2 * w.ways) >= 4 &&
+           (w.ways < 4 || w.tiles * w.mt <= 8))
+        w.ways *= 2;
     w.slices = 1;
     w.groups = 1;
     w.bytes = 0;
@@ -597,7 +605,8 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
     const AdapterPlan plan = adapter_plan(*p);
     if (adapter_tensor_path(*p, plan, x, w, a, b)) {
         CUtensorMap mapw, mapx, mapa, mapb, maps;
-        const bool few = p->T <= kFewProjTokens && plan.low_rows && static_cast<size_t>(p->T) * p->K * 2 <= kFewSmem;
+        const bool few = p->T <= kFewProjTokens && plan.low_rows &&
+                         static_cast<long long>(p->T) * p->N * p->K <= kFewProjProducts && static_cast<size_t>(p->T) * p->K * 2 <= kFewSmem;
         if (!few && (!encode_map(&mapw, w, p->K, p->N, 0, 128) || !encode_map(&mapx, x, p->K, p->T, 0, plan.nt)))
             return MR_ECUDA;
         AdapterArgs d;
@@ -618,13 +627,15 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
         d.ways = plan.ways;
         d.slices = plan.slices;
         wait_test(&d.tries, &d.drop);
+        const bool fused = few && p->T == 1 && p->n_adapters > 0 && static_cast<long long>(p->rank) * p->K <= kFusedLowProducts;
+        if (fused) return from_cuda(launch_adapter_few(x, w, a, true, p->out_dtype == MR_F32, d, st));
         if (p->n_adapters > 0 && plan.low_rows) {
             if (launch_adapter_low_rows(x, a, d, st) != cudaSuccess) return MR_ECUDA;
         } else if (p->n_adapters > 0) {
             if (!encode_map(&mapa, a, p->K, p->rank, p->n_adapters, p->rank)) return MR_ECUDA;
             if (launch_adapter_low(plan.nt, mapa, mapx, d, plan.groups, st) != cudaSuccess) return MR_ECUDA;
         }
-        if (few) return from_cuda(launch_adapter_few(x, w, p->out_dtype == MR_F32, d, st));
+        if (few) return from_cuda(launch_adapter_few(x, w, a, false, p->out_dtype == MR_F32, d, st));
         mapb = mapw;  // not read without adapters or by narrow tiles
         maps = mapw;
         if (p->n_adapters > 0 && plan.nt > 64) {

@@ -76,7 +76,8 @@ struct AdapterArgs {
 int launch_adapter_low(int nt, const CUtensorMap& map_a, const CUtensorMap& map_x, const AdapterArgs& a, int groups,
                        cudaStream_t st);
 int launch_adapter_low_rows(const void* x, const void* wa, const AdapterArgs& a, cudaStream_t st);
-int launch_adapter_few(const void* x, const void* w, bool f32, const AdapterArgs& a, cudaStream_t st);
+int launch_adapter_few(const void* x, const void* w, const void* wa, bool fused, bool f32, const AdapterArgs& a,
+                       cudaStream_t st);
 int launch_adapter_split(int nt, const AdapterArgs& a, cudaStream_t st);
 int launch_adapter_proj(int nt, bool f32, const CUtensorMap& map_w, const CUtensorMap& map_x, const CUtensorMap& map_b,
                         const CUtensorMap& map_s, const AdapterArgs& a, cudaStream_t st);
