@@ -889,7 +889,7 @@ int launch_proj(const CUtensorMap& map_w, const CUtensorMap& map_x, const CUtens
                 AdapterArgs a, cudaStream_t st)
 {
     const int rank = a.n_adapters > 0 ? a.rank : 0;
-    a.stages = stages_for(NT, rank, NT > kSmallTile ? 212 * 1024 : kProjBudget);
+    a.stages = stages_for(NT, rank, NT > kSmallTile ? 226 * 1024 : kProjBudget);
     const size_t smem = adapter_layout(NT, a.stages, rank).bytes;
     const void* f = reinterpret_cast<const void*>(&k_adapter_proj<NT, OutT>);
     const int e = ensure_smem(f, smem);
