@@ -402,3 +402,75 @@ def test_binding_refuses(mr):
         mr.adapter_proj(*y, out_dtype=torch.float16)
     with pytest.raises(ValueError):
         mr.adapter_proj(y[0], y[1], y[2], y[3], y[4][:3], y[5])
+
+
+def test_bounded_waits_give_up_and_report_it(mr):
+    """With the copies left out every wait of the tensor-core kernels runs out: the call's status says so (the
+    library's word for a call without one), and the next normal call is right."""
+    x, idx, w, w13, w2 = [t.cuda() for t in make_experts(40, 8, 4, 128, 64)]
+    big = [t.cuda() for t in make_experts(3000, 2, 2, 128, 64)]
+    want = [mr.experts(*v) for v in ((x, idx, w, w13, w2), big)]
+    projections = [[t.cuda() for t in make_adapters(T, K, N, 16, 3)] for T, K, N in ((20, 1024, 128), (300, 128, 256))]
+    wide = [t.cuda() for t in make_adapters(40000, 64, 128, 64, 2)]
+    projections.append(wide)
+    right = [mr.adapter_proj(*v) for v in projections]
+    assert mr.device_status(clear=True) == 0
+    mr.moe_router_set_wait_test(4, 1)
+    try:
+        for call in [lambda s: mr.experts(x, idx, w, w13, w2, status=s), lambda s: mr.experts(*big, status=s)] + [
+                lambda s, v=v: mr.adapter_proj(*v, status=s) for v in projections]:
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            call(status)
+            assert int(status.item()) == mr.MR_ETIMEOUT
+            assert mr.device_status() == 0
+        mr.experts(x, idx, w, w13, w2)
+        assert mr.device_status(clear=True) == mr.MR_ETIMEOUT
+    finally:
+        mr.moe_router_set_wait_test(0, 0)
+    assert torch.equal(mr.experts(x, idx, w, w13, w2), want[0]) and torch.equal(mr.experts(*big), want[1])
+    for v, r in zip(projections, right):
+        assert torch.equal(mr.adapter_proj(*v), r)
+    assert mr.device_status() == 0
+
+
+def test_two_graphs_beside_one_another(mr):
+    """Two captured steps, each with the workspaces of its own capture, replayed on two streams at once."""
+    E, k, H, I = 64, 4, 256, 128
+    graphs, wants = [], []
+    side = torch.cuda.Stream()
+    for T in (40, 300):
+        v = step_inputs(T, E, k, H, I, seed=T)
+        with torch.cuda.stream(side):
+            want = decode_step(mr, *v, k)[1]["out"].clone()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = decode_step(mr, *v, k)[1]["out"]
+        graphs.append((g, got, v))
+        wants.append(want)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (g, _, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, got, _), want in zip(graphs, wants):
+        assert torch.equal(got, want)
+
+
+def test_a_workspace_of_any_contents_is_reused(mr):
+    """One workspace for calls of other sizes, one after the other on one stream, eagerly and without a wait."""
+    sizes = [(1, 8, 2, 64, 32), (40, 16, 4, 128, 64), (700, 4, 2, 128, 64), (9, 5, 3, 33, 17), (3000, 2, 2, 64, 64)]
+    ins = [[t.cuda() for t in make_experts(*s, seed=i)] for i, s in enumerate(sizes)]
+    want = [mr.experts(*v) for v in ins]
+    ps = [mr.mr_expert_params(T, H, I, E, k, mr.MR_BF16, mr.MR_SILU) for T, E, k, H, I in sizes]
+    nb = max(mr.moe_experts_workspace_bytes(p) for p in ps)
+    ws = torch.full((nb,), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(v[0]) for v in ins]
+    for _ in range(4):
+        for p, (x, idx, w, w13, w2), o in zip(ps, ins, outs):
+            mr.moe_experts_fwd(p, x, idx, w, w13, w2, o, ws, nb)
+    torch.cuda.synchronize()
+    for o, r in zip(outs, want):
+        assert torch.equal(o, r)

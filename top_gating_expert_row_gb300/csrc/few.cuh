@@ -75,58 +75,53 @@ __device__ __forceinline__ uint4 load_weights(const uint4* p)
     return v;
 }
 
-// h of every pair; x in shared memory.
+// h of every pair; x in shared memory. A warp takes ROWS neighbouring rows at a
+// time, so that short rows (H of 1024 and less) keep as many loads in flight.
+template <int ROWS>
 __device__ __forceinline__ void few_up(const FewArgs& a, const int32_t* s_idx, const unsigned char* s_x)
 {
-    constexpr int kChunks = 8;  // 16-byte chunks of both rows in flight a lane
-    const int lane = threadIdx.x & 31, P = a.T * a.topk, H8 = a.H / 8;
+    constexpr int kChunks = 8 / ROWS;  // 16-byte chunks of each row in flight a lane
+    const int lane = threadIdx.x & 31, P = a.T * a.topk, H8 = a.H / 8, groups = (a.I + ROWS - 1) / ROWS;
     const int warps = gridDim.x * kFewWarps;
-    for (long long u = static_cast<long long>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5); u < static_cast<long long>(P) * a.I;
-         u += warps) {
-        const int p = static_cast<int>(u / a.I), i = static_cast<int>(u - static_cast<long long>(p) * a.I);
+    for (int u = blockIdx.x * kFewWarps + (threadIdx.x >> 5); u < P * groups; u += warps) {
+        const int p = u / groups, i0 = (u - p * groups) * ROWS;
         const int e = s_idx[p];
         if (e < 0 || e >= a.E) continue;
-        const uint4* g = reinterpret_cast<const uint4*>(a.w13 + (static_cast<long long>(e) * 2 * a.I + i) * a.H);
+        const uint4* g = reinterpret_cast<const uint4*>(a.w13 + (static_cast<long long>(e) * 2 * a.I + i0) * a.H);
         const uint4* v = g + static_cast<long long>(a.I) * H8;
         const uint4* x = reinterpret_cast<const uint4*>(s_x) + p / a.topk * H8;
-        float sg = 0.0f, sv = 0.0f;
+        float sg[ROWS] = {}, sv[ROWS] = {};
         for (int c0 = lane; c0 < H8; c0 += 32 * kChunks) {
-            uint4 wg[kChunks], wv[kChunks];
+            uint4 wg[kChunks][ROWS], wv[kChunks][ROWS];
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-                if (c0 + c * 32 < H8) {
-                    wg[c] = load_weights(g + c0 + c * 32);
-                    wv[c] = load_weights(v + c0 + c * 32);
-                }
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r)
+                    if (c0 + c * 32 < H8 && i0 + r < a.I) {
+                        wg[c][r] = load_weights(g + r * H8 + c0 + c * 32);
+                        wv[c][r] = load_weights(v + r * H8 + c0 + c * 32);
+                    }
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
                 if (c0 + c * 32 < H8) {
                     const uint4 xc = x[c0 + c * 32];
-                    sg = dot8(wg[c], xc, sg);
-                    sv = dot8(wv[c], xc, sv);
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+                        if (i0 + r < a.I) {
+                            sg[r] = dot8(wg[c][r], xc, sg[r]);
+                            sv[r] = dot8(wv[c][r], xc, sv[r]);
+                        }
                 }
         }
-        sg = warp_sum(sg);
-        sv = warp_sum(sv);
-        if (lane == 0) a.h[u] = act_f32(sg, a.act) * sv;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const float gs = warp_sum(sg[r]), vs = warp_sum(sv[r]);
+            if (lane == 0 && i0 + r < a.I) a.h[static_cast<long long>(p) * a.I + i0 + r] = act_f32(gs, a.act) * vs;
+        }
     }
 }
 
-// This warp's weights of `up`, to L2 at once: a warp holds one row pair's
-// loads in flight and has a few of them one after the other.
-__device__ __forceinline__ void few_up_prefetch(const FewArgs& a, const int32_t* s_idx)
-{
-    const int lane = threadIdx.x & 31, warps = gridDim.x * kFewWarps;
-    const long long first = static_cast<long long>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5);
-    // lanes 0, 1: the first row pair is loaded at once; from lane 2 on, the next ones
-    const long long u = first + static_cast<long long>(lane >> 1) * warps;
-    if (lane >= 2 && u < static_cast<long long>(a.T) * a.topk * a.I) {
-        const int p = static_cast<int>(u / a.I), i = static_cast<int>(u - static_cast<long long>(p) * a.I);
-        const int e = s_idx[p];
-        if (e >= 0 && e < a.E)
-            prefetch_l2(a.w13 + (static_cast<long long>(e) * 2 * a.I + i + (lane & 1 ? a.I : 0)) * a.H, a.H * 2);
-    }
-}
+__host__ __device__ inline int few_rows(int H) { return H <= 512 ? 4 : H <= 1024 ? 2 : 1; }
 
 // This warp's weights of `down`, to L2.
 __device__ __forceinline__ void few_down_prefetch(const FewArgs& a, const int32_t* s_idx)
@@ -205,8 +200,10 @@ __device__ __forceinline__ void few_body(const FewArgs& a, unsigned char* smem, 
     choose(s_idx, s_w);
     __syncthreads();
     if (!DOWN) {
-        few_up_prefetch(a, s_idx);
-        few_up(a, s_idx, s_v);
+        const int rows = few_rows(a.H);
+        if (rows == 4) few_up<4>(a, s_idx, s_v);
+        else if (rows == 2) few_up<2>(a, s_idx, s_v);
+        else few_up<1>(a, s_idx, s_v);
     } else {
         few_down_prefetch(a, s_idx);
         pdl_trigger();

@@ -81,7 +81,8 @@ int MR_CAT(launch_layer_few, MR_SUFFIX)(const RouteArgs& r, const FewArgs& a, in
     const size_t smem = few_smem(a, down, static_cast<size_t>(L.bytes) * std::min(a.T, kFewWarps));
     const int e = ensure_smem(reinterpret_cast<const void*>(f), smem);
     if (e != cudaSuccess) return e;
-    const long long tasks = down ? static_cast<long long>(a.T) * a.H : static_cast<long long>(a.T) * a.topk * a.I;
+    const long long tasks = down ? static_cast<long long>(a.T) * a.H
+                                 : static_cast<long long>(a.T) * a.topk * ((a.I + few_rows(a.H) - 1) / few_rows(a.H));
     const int grid = persistent_grid(reinterpret_cast<const void*>(f), kFewThreads, smem, (tasks + kFewWarps - 1) / kFewWarps);
     if (grid < 1) return cudaErrorLaunchOutOfResources;
     return launch_kernel(f, dim3(grid), dim3(kFewThreads), smem, st, 0, r, a);
