@@ -94,26 +94,26 @@ int ensure_smem(const void* func, size_t bytes)
     return cudaSuccess;
 }
 
-bool cluster_fits(const void* func, int threads, size_t smem, int cs)
+int active_clusters(const void* func, int threads, size_t smem, int cs)
 {
     struct Entry {
         const void* func;
         size_t smem;
         int dev, cs;
-        bool fits;
+        int clusters;
     };
     static std::mutex mu;
-    static Entry cache[64];
+    static Entry cache[128];
     static int n = 0;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     {
         std::lock_guard<std::mutex> lk(mu);
         for (int i = 0; i < n; ++i)
             if (cache[i].func == func && cache[i].smem == smem && cache[i].dev == dev && cache[i].cs == cs)
-                return cache[i].fits;
+                return cache[i].clusters;
     }
-    bool fits = false;
+    int clusters = 0;
     int maxsm = 0;
     if (cudaDeviceGetAttribute(&maxsm, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) == cudaSuccess &&
         smem <= static_cast<size_t>(maxsm) && ensure_smem(func, smem) == cudaSuccess &&
@@ -129,13 +129,17 @@ bool cluster_fits(const void* func, int threads, size_t smem, int cs)
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        int clusters = 0;
-        fits = cudaOccupancyMaxActiveClusters(&clusters, func, &cfg) == cudaSuccess && clusters >= 1;
+        if (cudaOccupancyMaxActiveClusters(&clusters, func, &cfg) != cudaSuccess) clusters = 0;
     }
     cudaGetLastError();  // a refused size is not an error of the call
     std::lock_guard<std::mutex> lk(mu);
-    if (n < 64) cache[n++] = Entry{func, smem, dev, cs, fits};
-    return fits;
+    if (n < 128) cache[n++] = Entry{func, smem, dev, cs, clusters};
+    return clusters;
+}
+
+bool cluster_fits(const void* func, int threads, size_t smem, int cs)
+{
+    return active_clusters(func, threads, smem, cs) >= 1;
 }
 
 // ---- per-(score, dtype) launchers defined in fwd.cu compilations --------------------------------

@@ -19,6 +19,8 @@
 // completes a token (a counter per token and row tile), it cost `down` a fence,
 // an atomic and a fence a unit, 4 us of latency that the next unit's products
 // did not cover (T=16 E=256 k=8: 83 us instead of 60; T=8192 E=8 k=2: 208 us).
+#include <algorithm>
+
 #include "experts.h"
 #include "gemm.cuh"
 
@@ -39,7 +41,7 @@ __host__ __device__ inline CtaLayout cta_layout(int nt, int stages)
     CtaLayout L;
     uint32_t o = 0;
     L.a = o; o += static_cast<uint32_t>(stages) * kRows * kStepBytes;
-    L.b = o; o += static_cast<uint32_t>(stages) * nt * kStepBytes;
+    L.b = o; o += static_cast<uint32_t>(stages) * (nt >= kPairColumns ? nt / 2 : nt) * kStepBytes;
     L.info = o; o += static_cast<uint32_t>(nt) * 8;
     o = (o + 15) / 16 * 16;
     L.bars = o; o += sizeof(GemmBars);
@@ -128,11 +130,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const CtaLayout L = cta_layout(NT, a.stages);
     GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr bool kPair = NT >= kPairColumns;
+    constexpr int kCtas = kPair ? 2 : 1;
+    const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
     constexpr uint32_t kColumns = 2 * NT;  // two accumulators: one fills while the other is read
-    constexpr uint32_t a_bytes = kRows * kStepBytes, b_bytes = NT * kStepBytes;
+    constexpr uint32_t a_bytes = kRows * kStepBytes, b_bytes = NT / kCtas * kStepBytes;
     const uint32_t ring_a = smem_addr(smem + L.a), ring_b = smem_addr(smem + L.b);
 
-    if (warp == 1) tmem_alloc(&bars.tmem, kColumns);
+    if (warp == 1) tmem_alloc<kPair>(&bars.tmem, kColumns);
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
             mbar_init(&bars.full[i], 2);
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.acc_full[i], 1);
-            mbar_init(&bars.acc_empty[i], kEpilogueThreads);
+            mbar_init(&bars.acc_empty[i], 4 * kCtas);  // a warp's arrival each, of both CTAs in the first one's
         }
         mbar_init(&bars.drained, 1);
         bars.gone = 0;
@@ -149,6 +154,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();  // the other CTA's barriers are ready
     tc_fence_after();
     const uint32_t tmem = bars.tmem;
 
@@ -160,7 +166,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const Waits wait{&bars.gone, a.tries};
     const uint32_t drain = min(a.tries, kDrainTries);
     const int nblk = min(__ldcg(a.npp), a.cap) / NT;
-    const int units = nblk * a.mt;
+    const int mts = (a.mt + kCtas - 1) / kCtas;  // row tiles, a pair's two as one (the last second one may be past the rows)
+    const int units = nblk * mts, first_unit = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
     const int ksteps = ((DOWN ? a.I : a.H) + kStepK - 1) / kStepK;
     RingPos pos;
     int issued = 0;
@@ -168,8 +175,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) {
         if (elect_one()) {
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const int b = u / a.mt, m = u - b * a.mt;
+            for (int u = first_unit; ok && u < units; u += stride) {
+                const int b = u / mts, m = (u - b * mts) * kCtas + rank;
                 const int e = min(max(__ldcg(a.eids + b), 0), a.E - 1);
                 for (int k = 0; k < ksteps; ++k) {
                     if (DOWN && issued == a.stages) pdl_wait();
@@ -177,16 +184,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (!ok) break;
                     uint64_t* full = &bars.full[pos.s];
                     const uint32_t dst = ring_a + pos.s * a_bytes;
-                    mbar_expect(full, a_bytes);
+                    // a pair's first CTA counts what both bring
+                    if (rank == 0) mbar_expect(full, a_bytes * kCtas);
                     ++issued;
                     if (!a.drop) {
+                        const uint32_t counted = kPair ? cluster_addr(full, 0) : 0;
+                        auto load = [&](uint32_t to, int row) {
+                            if (kPair) load_box3_pair(to, &map_w, k * kStepK, row, e, counted);
+                            else load_box3(to, &map_w, k * kStepK, row, e, full);
+                        };
                         if (DOWN) {
-                            load_box3(dst, &map_w, k * kStepK, m * kRows, e, full);
+                            load(dst, m * kRows);
                         } else {
                             const int i = m * (kRows / 2);
                             for (int g = 0; g < kRows / 32; ++g) {
-                                load_box3(dst + g * 32 * kStepBytes, &map_w, k * kStepK, i + g * 16, e, full);
-                                load_box3(dst + (g * 32 + 16) * kStepBytes, &map_w, k * kStepK, a.I + i + g * 16, e, full);
+                                load(dst + g * 32 * kStepBytes, i + g * 16);
+                                load(dst + (g * 32 + 16) * kStepBytes, a.I + i + g * 16);
                             }
                         }
                     }
@@ -202,11 +215,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         constexpr bool kScattered = !DOWN && NT < kGatherColumns;
         const int box = kTokenBox<NT>;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const int b = u / a.mt;
+        for (int u = first_unit; ok && u < units; u += stride) {
+            const int b = u / mts;
             const int32_t* ids = a.sids + static_cast<long long>(b) * NT;
             const int n = block_pairs<NT>(ids, a.P, lane);
-            const int cols = max((n + 15) & ~15, 16), boxes = (cols + box - 1) / box;
+            // (a pair's CTAs bring half of the columns' tokens each)
+            constexpr int kRound = 16 * kCtas;
+            const int cols = max((n + kRound - 1) / kRound, 1) * kRound, boxes = (cols / kCtas + box - 1) / box;
             int4 row[kScattered ? NT / 4 : 1];
             if (kScattered) {
 #pragma unroll
@@ -224,7 +239,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     uint64_t* full = &bars.full[pos.s];
                     const uint32_t dst = ring_b + pos.s * b_bytes;
                     if (k == 0) bars.cols[pos.s] = cols;
-                    mbar_expect(full, (kScattered ? cols : boxes * box) * kStepBytes);
+                    if (rank == 0) mbar_expect(full, (kScattered ? cols : boxes * box * kCtas) * kStepBytes);
                     ++issued;
                     if (!a.drop) {
                         if (kScattered) {
@@ -232,8 +247,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             for (int g = 0; g < NT / 4; ++g)
                                 if (g * 4 < cols) load_rows4(dst + g * 4 * kStepBytes, &map_t, k * kStepK, row[g], full);
                         } else {
-                            for (int g = 0; g < boxes; ++g)
-                                load_box2(dst + g * box * kStepBytes, &map_t, k * kStepK, b * NT + g * box, full);
+                            const int first = b * NT + rank * (cols / kCtas);
+                            for (int g = 0; g < boxes; ++g) {
+                                const uint32_t to = dst + g * box * kStepBytes;
+                                if (kPair) load_box2_pair(to, &map_t, k * kStepK, first + g * box, cluster_addr(full, 0));
+                                else load_box2(to, &map_t, k * kStepK, first + g * box, full);
+                            }
                         }
                     }
                     pos.next(a.stages);
@@ -245,12 +264,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             ok = __all_sync(kFull, ok);
         }
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
             if (DOWN) pdl_wait();
             int seen = 0;
             bool ok = true;
             StagePoll poll;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++seen) {
+            for (int u = first_unit; ok && u < units; u += stride, ++seen) {
                 const int buf = seen & 1;
                 ok = seen < 2 || wait(&bars.acc_empty[buf], ((seen >> 1) - 1) & 1);
                 if (!ok) break;
@@ -261,17 +280,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     ok = poll.take(wait, bars, pos, a.stages);
                     if (!ok) break;
                     tc_fence_after();
-                    if (k == 0) desc = product_desc(bars.cols[pos.s]);
+                    if (k == 0) desc = product_desc(bars.cols[pos.s], kPair);
                     const uint64_t da = operand_desc(ring_a + pos.s * a_bytes), db = operand_desc(ring_b + pos.s * b_bytes);
 #pragma unroll
-                    for (int q = 0; q < kStepK / 16; ++q) mma16(d, da + q * 2, db + q * 2, desc, k > 0 || q > 0);
-                    mma_commit(&bars.empty[pos.s]);
+                    for (int q = 0; q < kStepK / 16; ++q) mma16<kPair>(d, da + q * 2, db + q * 2, desc, k > 0 || q > 0);
+                    if (kPair) mma_commit_pair(&bars.empty[pos.s], 3);
+                    else mma_commit(&bars.empty[pos.s]);
                     pos.next(a.stages);
                 }
-                if (ok) mma_commit(&bars.acc_full[buf]);
+                if (ok && kPair) mma_commit_pair(&bars.acc_full[buf], 3);
+                else if (ok) mma_commit(&bars.acc_full[buf]);
             }
             if (!ok) {
-                mma_commit(&bars.drained);
+                if (kPair) mma_commit_pair(&bars.drained, 1);
+                else mma_commit(&bars.drained);
                 mbar_wait(&bars.drained, 0, drain);
             }
         }
@@ -281,8 +303,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         int* info = reinterpret_cast<int*>(smem + L.info);  // NT pair ids, NT weights
         float* info_w = reinterpret_cast<float*>(info + NT);
         int seen = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++seen) {
-            const int b = u / a.mt, m = u - b * a.mt, buf = seen & 1;
+        for (int u = first_unit; u < units; u += stride, ++seen) {
+            const int b = u / mts, m = (u - b * mts) * kCtas + rank, buf = seen & 1;
             const int32_t* ids = a.sids + static_cast<long long>(b) * NT;
             const int n = block_pairs<NT>(ids, a.P, lane);
             if (DOWN) {
@@ -307,7 +329,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             a.y[static_cast<long long>(info[c0 + c]) * a.H + row] = v[c] * info_w[c0 + c];
                 }
                 tc_fence_before();
-                mbar_arrive(&bars.acc_empty[buf]);
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_cluster(cluster_addr(&bars.acc_empty[buf], 0));
+                    else mbar_arrive(&bars.acc_empty[buf]);
+                }
                 epilogue_sync();  // the next unit overwrites info
             } else {
                 // lanes 0-15 hold gate rows, lanes 16-31 the same up rows: the
@@ -328,16 +354,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                     }
                 tc_fence_before();
-                mbar_arrive(&bars.acc_empty[buf]);
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair) mbar_arrive_cluster(cluster_addr(&bars.acc_empty[buf], 0));
+                    else mbar_arrive(&bars.acc_empty[buf]);
+                }
             }
         }
     }
     __syncwarp();
     tc_fence_before();
+    if (kPair) cluster_sync();  // no CTA leaves while the other may use its memory or its barriers
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_free(tmem, kColumns);
+        tmem_free<kPair>(tmem, kColumns);
     }
     if (threadIdx.x == 0 && bars.gone) report_status(a.status, kStatusTimeout);
 }
@@ -377,9 +408,11 @@ int launch_one(const CUtensorMap& map_w, const CUtensorMap& map_t, ExpertArgs a,
     const void* f = reinterpret_cast<const void*>(&k_experts<NT, DOWN>);
     const int e = ensure_smem(f, smem);
     if (e != cudaSuccess) return e;
-    const int grid = persistent_grid(f, kGemmThreads, smem, units);
+    constexpr int kCtas = NT >= kPairColumns ? 2 : 1;
+    const int grid = kCtas == 1 ? persistent_grid(f, kGemmThreads, smem, units)
+                                : 2 * static_cast<int>(std::min<long long>(active_clusters(f, kGemmThreads, smem, 2), (units + 1) / 2));
     if (grid < 1) return cudaErrorLaunchOutOfResources;
-    return launch_kernel(&k_experts<NT, DOWN>, dim3(grid), dim3(kGemmThreads), smem, st, 0, map_w, map_t, a);
+    return launch_kernel(&k_experts<NT, DOWN>, dim3(grid), dim3(kGemmThreads), smem, st, kCtas == 2 ? 2 : 0, map_w, map_t, a);
 }
 
 template <bool DOWN>

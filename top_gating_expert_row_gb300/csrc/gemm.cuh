@@ -13,6 +13,11 @@
 // step shorter: its four products take 280 clocks at any width up to 128 columns
 // (measured; 537 at 256), 16 KB of weights in 0.15 us, twice what an SM's share
 // of the memory brings in that time. Few units are split over K instead.
+//
+// Prompts (tiles of 256 tokens): a pair of CTAs makes one product of 256 rows,
+// each holding 128 rows of the weights and half of the tokens (cta_group::2). A
+// k-step then brings an SM 32 KB instead of 48, and what an SM takes in, 64 to 70
+// bytes a clock, bounds such steps (48 KB: 389 ns a step of 280).
 #pragma once
 
 #include <cuda.h>
@@ -24,7 +29,8 @@ namespace mr {
 constexpr int kGemmThreads = 256;   // warp 0 weights, 1 products, 2 tokens, 3 spare, 4-7 epilogue
 constexpr int kEpilogueThreads = 128;
 constexpr int kMaxStages = 16;
-constexpr int kRows = 128;          // weight rows of a unit
+constexpr int kRows = 128;          // weight rows of a CTA's unit
+constexpr int kPairColumns = 256;   // tiles of this many tokens are taken by pairs of CTAs
 constexpr int kStepBytes = 128;     // one row of a k-step
 constexpr int kStepK = 64;
 
@@ -120,6 +126,19 @@ struct RingPos {
     }
 };
 
+// The cluster address of this variable in CTA `rank`, and an arrival at a barrier there.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // A named barrier of the epilogue warps.
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -147,6 +166,26 @@ __device__ __forceinline__ void load_box2(uint32_t dst, const CUtensorMap* m, in
         : "memory");
 }
 
+// The same for a pair of CTAs: into this CTA's memory, counted by a barrier of
+// either one (a cluster address).
+__device__ __forceinline__ void load_box3_pair(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void load_box2_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(m), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
 // Four rows of a matrix, one after the other in shared memory (the map's box is one row).
 __device__ __forceinline__ void load_rows4(uint32_t dst, const CUtensorMap* m, int x, int4 r, uint64_t* bar)
 {
@@ -159,16 +198,28 @@ __device__ __forceinline__ void load_rows4(uint32_t dst, const CUtensorMap* m, i
 
 // ---- tensor memory and products ----------------------------------------------------------------------------------
 
-// All lanes of one warp; `slot` (shared) receives the address.
+// All lanes of one warp (PAIR: of one warp in each CTA); `slot` (shared) receives the address.
+template <bool PAIR = false>
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t columns)
 {
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        return;
+    }
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(columns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
 
+template <bool PAIR = false>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns)
 {
+    if (PAIR) {
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+        return;
+    }
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 
@@ -182,15 +233,26 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr)
     return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// bf16 x bf16 -> fp32, 128 rows, n columns (a multiple of 16), both operands K-major.
-__device__ __forceinline__ uint32_t product_desc(int n)
+// bf16 x bf16 -> fp32, 128 rows (a pair's: 256), n columns (a multiple of 16; a
+// pair's: of 32), both operands K-major.
+__device__ __forceinline__ uint32_t product_desc(int n, bool pair = false)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((pair ? 16u : 8u) << 24);
 }
 
-// D (+)= A B^T over 16 of K.
+// D (+)= A B^T over 16 of K. PAIR: issued by the pair's first CTA for both; each
+// has its rows of A, its half of B's rows and its rows of D at these addresses.
+template <bool PAIR = false>
 __device__ __forceinline__ void mma16(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add)
 {
+    if (PAIR) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(desc), "r"(add ? 1u : 0u)
+            : "memory");
+        return;
+    }
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
@@ -203,6 +265,16 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
+}
+
+// The same for a pair's products, at this barrier of the CTAs in `mask`.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"(mask)
+        : "memory");
 }
 
 // 16 consecutive columns of this warp's 32 rows: the lane's row.

@@ -252,5 +252,7 @@ int ensure_smem(const void* func, size_t smem);
 // shared-memory limit and, for cs > 8, allows non-portable cluster sizes.
 // Cached.
 bool cluster_fits(const void* func, int threads, size_t smem, int cs);
+// How many such clusters run at a time (0: none fits). Sets the same limits. Cached.
+int active_clusters(const void* func, int threads, size_t smem, int cs);
 
 }  // namespace mr
