@@ -240,16 +240,19 @@ size_t part(size_t& o, size_t bytes)
 // Units that keep the SMs busy (one CTA each).
 constexpr int kFullGrid = 148;
 
-// Columns (pairs) of a block: four times the mean load of an expert that has any, so
-// that few experts need a second block (which reads their weights again). A
-// product only takes the columns that its block fills, so wide blocks cost
-// shared memory, not time.
+// Columns (pairs) of a block: four times the mean load of an expert that has any,
+// up to 128, so that few experts need a second block (which reads their weights
+// again); twice and eight times are slower (T=512 E=384+1 k=9 with skewed loads:
+// 110 and 106 us against 104). A product only takes the columns that its block
+// fills, so wide blocks cost shared memory, not time. 256, which pairs of CTAs
+// take, from a mean of 112 on: at 100 113.9 us against 110.8 with 128 (E=32 k=2
+// H=2048 I=1024), at 150 123.7 against 131.6.
 int columns_for(long long P, int E)
 {
-    const long long load = 4 * ((P + std::min<long long>(P, E) - 1) / std::min<long long>(P, E));
+    const long long active = std::min<long long>(P, E), load = (P + active - 1) / active;
     int nt = 16;
-    while (nt < 256 && nt < load) nt *= 2;
-    return nt;
+    while (nt < 128 && nt < 4 * load) nt *= 2;
+    return load > 112 ? 256 : nt;
 }
 
 // route: the routing options when the call routes too (room for its outputs and workspace)
