@@ -353,6 +353,18 @@ def test_captured_and_replayed_on_new_inputs(mr, T):
         assert torch.equal(got["topk_idx"], wg["topk_idx"])
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 24, 3, 192, 72), (29, 24, 3, 192, 72), (900, 6, 3, 192, 72)])
+def test_a_shapes_first_call_is_captured(mr, T, E, k, H, I):
+    v = step_inputs(T, E, k, H, I, seed=9)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        logits, got = decode_step(mr, *v, k)
+    graph.replay()
+    torch.cuda.synchronize()
+    wl, wg = decode_step(mr, *v, k)
+    assert torch.equal(logits, wl) and torch.equal(got["out"], wg["out"])
+
+
 def test_two_streams_at_once(mr):
     """Calls on two streams, each with its own workspace, beside one another."""
     E, k, H, I = 64, 4, 256, 128

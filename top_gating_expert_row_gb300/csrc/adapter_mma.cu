@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         prefetch_map(&map_x);
     }
     pdl_wait();
-    pdl_trigger();
     // the distinct adapters of the tile
     for (int t = threadIdx.x; t < NT; t += kGemmThreads) {
         const int id = t < tokens ? __ldcg(a.adapter + t0 + t) : -1;
@@ -108,6 +107,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         slot[t] = id >= 0 && id < a.n_adapters ? id : -1;
     }
     __syncthreads();
+    pdl_trigger();  // after this CTA has its tensor memory: the next kernel takes some too, and waits for this one
     // a token is its adapter's first if no earlier one names it (the previous
     // one does, mostly); the first ones are listed in order
     int id = -1;

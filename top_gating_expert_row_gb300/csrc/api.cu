@@ -27,14 +27,14 @@ struct OccEntry {
 };
 std::mutex g_occ_mu;
 OccEntry g_occ[128];
-int g_occ_n = 0;
+int g_occ_n = 0, g_occ_next = 0;
 
 struct SmemEntry {
     const void* func;
     int device;
     size_t bytes;
 };
-SmemEntry g_smem[128];
+SmemEntry g_smem[512];
 int g_smem_n = 0;
 
 int g_sm_count[64] = {0};
@@ -55,7 +55,10 @@ int persistent_grid(const void* func, int threads, size_t smem, long long units,
         if (g_occ[i].func == func && g_occ[i].smem == smem && g_occ[i].device == dev) blocks = g_occ[i].blocks;
     if (blocks < 0) {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, func, threads, smem) != cudaSuccess) return -1;
-        if (g_occ_n < 128) g_occ[g_occ_n++] = OccEntry{func, smem, dev, blocks};
+        // full: the oldest entry makes room (sizes of shared memory vary from call to call)
+        g_occ[g_occ_next] = OccEntry{func, smem, dev, blocks};
+        g_occ_next = (g_occ_next + 1) % 128;
+        if (g_occ_n < 128) ++g_occ_n;
     }
     if (blocks < 1) return -1;
     const long long cap = static_cast<long long>(blocks) * g_sm_count[dev];
@@ -90,7 +93,7 @@ int ensure_smem(const void* func, size_t bytes)
     e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
     if (ent) ent->bytes = bytes;
-    else if (g_smem_n < 128) g_smem[g_smem_n++] = SmemEntry{func, dev, bytes};
+    else if (g_smem_n < 512) g_smem[g_smem_n++] = SmemEntry{func, dev, bytes};
     return cudaSuccess;
 }
 
@@ -104,7 +107,7 @@ int active_clusters(const void* func, int threads, size_t smem, int cs)
     };
     static std::mutex mu;
     static Entry cache[128];
-    static int n = 0;
+    static int n = 0, next = 0;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     {
@@ -133,7 +136,9 @@ int active_clusters(const void* func, int threads, size_t smem, int cs)
     }
     cudaGetLastError();  // a refused size is not an error of the call
     std::lock_guard<std::mutex> lk(mu);
-    if (n < 128) cache[n++] = Entry{func, smem, dev, cs, clusters};
+    cache[next] = Entry{func, smem, dev, cs, clusters};
+    next = (next + 1) % 128;
+    if (n < 128) ++n;
     return clusters;
 }
 

@@ -276,9 +276,10 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     w.sort_bytes = moe_sort_workspace_bytes(p.T, p.topk, p.E, w.nt);
     if (route) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
     w.sort = part(o, w.sort_bytes);
-    w.h = part(o, std::max(cap, 2 * P) * p.I * 2);  // few pairs: fp32
-    w.xs = part(o, w.nt >= kGatherColumns ? cap * p.H * 2 : 0);
-    w.y = part(o, P * p.H * 4);
+    const bool whole = p.H % 8 == 0 && p.I % 8 == 0;  // else the plain kernels
+    w.h = part(o, (whole ? std::max(cap, 2 * P) : P) * p.I * 2);  // few pairs: fp32
+    w.xs = part(o, whole && w.nt >= kGatherColumns ? cap * p.H * 2 : 0);
+    w.y = part(o, whole ? P * p.H * 4 : 0);
     w.bytes = o;
     return w;
 }
@@ -343,12 +344,12 @@ int launch_layer_few(const mr_router_params* p, const RouteArgs& r, const FewArg
 }
 
 // Whether the tensor-core kernels' copies can address these arrays: 16-byte
-// aligned bases and row strides.
+// aligned bases and row strides, an expert's weights below 2^40 bytes.
 bool tensor_path(const mr_expert_params& p, const ExpertPlan& plan, const void* x, const void* w13, const void* w2)
 {
     const long long blocks = plan.cap / plan.nt + 1;
     return plan.cap > 0 && p.H % 8 == 0 && p.I % 8 == 0 && aligned(x, 16) && aligned(w13, 16) && aligned(w2, 16) &&
-           blocks * std::max(plan.mt_up, plan.mt_down) < INT_MAX;
+           static_cast<long long>(p.I) * p.H < (1ll << 37) && blocks * std::max(plan.mt_up, plan.mt_down) < INT_MAX;
 }
 
 int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx, const float* w, const void* w13,
@@ -405,7 +406,7 @@ struct AdapterPlan {
 
 // Rank-space values: up to this many products a warp per four of them, above
 // it the tensor cores.
-constexpr long long kLowRowsProducts = 64ll << 20;
+constexpr double kLowRowsProducts = 64 << 20;
 // What the projection on the CUDA cores takes: up to 4 tokens, and products up
 // to T*N*K = 10M (T=1 K=4096: 7.0 us against 7.7 on the tensor cores at N=2048,
 // 11.5 against 8.6 at N=4096; T=2 K=N=2048: 6.7 against 7.5).
@@ -422,8 +423,9 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
     w.nt = 16;
     while (w.nt < 64 && w.nt < p.T) w.nt *= 2;
     const long long mt = (p.N + 127) / 128;
-    while (p.out_dtype == MR_BF16 && w.nt >= 64 && w.nt < 256 && (p.T + 2 * w.nt - 1) / (2 * w.nt) * mt >= kFullGrid) w.nt *= 2;
-    w.tiles = (p.T + w.nt - 1) / w.nt;
+    const long long T = p.T;
+    while (p.out_dtype == MR_BF16 && w.nt >= 64 && w.nt < 256 && (T + 2 * w.nt - 1) / (2 * w.nt) * mt >= kFullGrid) w.nt *= 2;
+    w.tiles = static_cast<int>((T + w.nt - 1) / w.nt);
     w.mt = static_cast<int>(mt);
     // a cluster shares a unit's sum over K while that gives idle SMs work
     // (clusters of 8 fit the GPU's partitions badly when there are many)
@@ -435,7 +437,7 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
     w.slices = 1;
     w.groups = 1;
     w.bytes = 0;
-    w.low_rows = static_cast<long long>(p.T) * p.rank * p.K <= kLowRowsProducts;
+    w.low_rows = static_cast<double>(T) * p.rank * p.K <= kLowRowsProducts;
     if (p.n_adapters == 0) return w;
     if (w.low_rows) {
         // slices of K while there are fewer warps than the SMs hold in flight
