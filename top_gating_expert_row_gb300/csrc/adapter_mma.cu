@@ -20,6 +20,13 @@
 // Calls with fewer units than SMs share each unit's sum over K among the CTAs
 // of a cluster, which add their parts through distributed shared memory.
 //
+// Measured (CUDA graph, one GB300): T=48 K=N=4096 rank 16, an adapter each, 14.4 us
+// (33.5 MB of w are 4.9 us; the rest is the chain rank-space values, b, cluster
+// sum); T=333 K=1544 N=1000 rank 8 16.4 us; T=4096 K=N=4096 rank 64 124 us, of it
+// the projection 101 (1.4 PFLOP/s; its 512 units are 4 rounds on 152 SMs where
+// 3.4 would do), the rank-space values 26 and their split 8 beside it; T=8 K=N=4096
+// rank 16 9.9 us.
+//
 // k_adapter_proj starts while k_adapter_low runs (its sum over K needs nothing
 // of it), so the low-rank product costs little time of its own once w is large.
 #include <type_traits>

@@ -11,6 +11,11 @@
 // tokens themselves (each CTA all of them: they are few, and it costs what
 // waiting for another launch would). `down` starts beside `up`, brings its
 // weights to L2 meanwhile and waits only for h.
+//
+// Measured (CUDA graph, states that do not fit L2): T=1 E=256 k=8 H=2048 I=768 22.0
+// us for 75 MB, 11.1 at the memory's rate; about 2 us of it routing, the rest
+// that a warp holds one row pair's loads in flight and has two or three pairs one
+// after the other. T=1 E=8 k=2 H=512 I=256 6.6 us, all latency.
 #pragma once
 
 #include "experts.h"
