@@ -313,8 +313,10 @@ typedef struct {
  * moe_experts_fwd -- the experts' products for a given choice of experts ([GEMM]
  * moe_gemm_2stage, the consumer of the sorted layout; the sort runs inside).
  *   for each token t and slot j with e = topk_idx[t][j] in [0, E):
- *     g = w13[e][0:I] x[t],  u = w13[e][I:2I] x[t],  h = act(g) * u  (rounded to bf16)
+ *     g = w13[e][0:I] x[t],  u = w13[e][I:2I] x[t],  h = act(g) * u
  *     out[t] = sum_j topk_w[t][j] * (w2[e] h_j)      (fp32, slots in ascending j)
+ * h is kept to 16 significant bits or more, or rounded to bf16 where experts have more
+ * than 16 pairs in the mean.
  * x [T x H], topk_idx int32 [T x topk], topk_w fp32 [T x topk], w13 [E x 2I x H] (gate
  * rows, then up rows), w2 [E x H x I], out [T x H]. out must not overlap an input.
  * Slots whose id is outside [0, E) contribute nothing (a token of such slots alone gets a

@@ -22,7 +22,7 @@
 //
 // Measured (CUDA graph, one GB300): T=48 K=N=4096 rank 16, an adapter each, 14.4 us
 // (33.5 MB of w are 4.9 us; the rest is the chain rank-space values, b, cluster
-// sum); T=333 K=1544 N=1000 rank 8 16.4 us; T=4096 K=N=4096 rank 64 124 us, of it
+// sum); T=333 K=1544 N=1000 rank 8 17.1 us; T=4096 K=N=4096 rank 64 124 us, of it
 // the projection 101 (1.4 PFLOP/s; its 512 units are 4 rounds on 152 SMs where
 // 3.4 would do), the rank-space values 26 and their split 8 beside it; T=8 K=N=4096
 // rank 16 9.9 us.
@@ -38,7 +38,7 @@ namespace mr {
 
 namespace {
 constexpr int kChunkRanks = 32;  // ranks of a further step (hi and lo)
-constexpr int kSegment = 8;      // k-steps between readings of the accumulator, fp32 output
+constexpr int kSegment = 4;      // k-steps between readings of the accumulator, fp32 output
 constexpr int kSmallTile = 64;   // tiles up to this keep the adapters' part of a whole unit in shared memory
 
 struct AdapterLayout {
@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(256) k_adapter_split(AdapterArgs a)
 // Output in fp32: the tensor cores add to their accumulator without rounding
 // the last bit, off by 2e-6 of the result at K = 4096, so it is taken out every
 // kSegment steps and the parts are summed in registers (tiles of at most 64
-// tokens, whose sums fit there). In bf16 one segment does.
+// tokens, whose sums fit there): 0.9e-6 at most over random sizes, 1.5e-6 with
+// parts twice as long, which are 4% faster. In bf16 one segment does.
 template <int NT, typename OutT>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_adapter_proj(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,

@@ -277,7 +277,8 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     if (route) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
     w.sort = part(o, w.sort_bytes);
     const bool whole = p.H % 8 == 0 && p.I % 8 == 0;  // else the plain kernels
-    w.h = part(o, (whole ? std::max(cap, 2 * P) : P) * p.I * 2);  // few pairs: fp32
+    // few pairs: fp32; narrow blocks: two parts
+    w.h = part(o, (whole ? std::max(w.nt <= kSplitColumns ? 2 * cap : cap, 2 * P) : P) * p.I * 2);
     w.xs = part(o, whole && w.nt >= kGatherColumns ? cap * p.H * 2 : 0);
     w.y = part(o, whole ? P * p.H * 4 : 0);
     w.bytes = o;
@@ -361,7 +362,7 @@ int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx,
     const int box = token_box(plan.nt);
     if (!encode_map(&map13, w13, p.H, 2ll * p.I, p.E, 16) ||
         !encode_map(&mapx, gather ? ws + plan.xs : x, p.H, gather ? plan.cap : p.T, 0, gather ? box : 1) ||
-        !encode_map(&map2, w2, p.I, p.H, p.E, 128) || !encode_map(&maph, ws + plan.h, p.I, plan.cap, 0, box))
+        !encode_map(&map2, w2, p.I, p.H, p.E, 128) || !encode_map(&maph, ws + plan.h, p.I, plan.nt <= kSplitColumns ? 2ll * plan.cap : plan.cap, 0, box))
         return MR_ECUDA;
     ExpertArgs a;
     a.x = static_cast<const __nv_bfloat16*>(x);

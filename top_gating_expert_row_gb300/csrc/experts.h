@@ -30,7 +30,7 @@ struct ExpertArgs {
     const int32_t* npp;    // rows of the sorted layout
     const int32_t* idx;    // [T][topk]
     const float* w;        // [T][topk]
-    __nv_bfloat16* h;      // [cap][I], in sorted order
+    __nv_bfloat16* h;      // [cap][I], in sorted order (narrow blocks: hi, then lo)
     float* y;              // [T * topk][H], weighted
     __nv_bfloat16* out;    // [T][H]
     int32_t* status;
@@ -43,6 +43,8 @@ struct ExpertArgs {
 
 // Blocks of this many pairs or more read x from a copy in sorted order.
 constexpr int kGatherColumns = 32;
+// Blocks of at most this many pairs keep h as two bf16 parts (16 significant bits).
+constexpr int kSplitColumns = 64;
 // Rows of one copy of the token operand.
 inline int token_box(int nt) { return nt >= 64 ? nt / 4 : 16; }
 

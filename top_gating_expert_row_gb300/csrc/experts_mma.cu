@@ -1,7 +1,8 @@
 // The experts' products on the tensor cores, over the sorted layout (blocks of
 // at most NT pairs of one expert).
 //
-//   k_experts_up    h[p][i] = act(w13[e][i] . x_t) * (w13[e][I + i] . x_t)
+//   k_experts_up    h[p][i] = act(w13[e][i] . x_t) * (w13[e][I + i] . x_t), as two bf16 parts (16
+//                   significant bits) in blocks of at most 64 pairs, else rounded to bf16
 //   k_experts_down  y[t][j] = weight * (w2[e] . h[p])
 //   k_experts_sum   out[t] = sum_j y[t][j], in slot order
 //
@@ -38,17 +39,25 @@ template <int NT>
 constexpr int kTokenBox = NT >= 64 ? NT / 4 : 16;
 }  // namespace
 
+// Rows of the token operand: h in two parts is twice as many columns, which cost
+// a product nothing up to 128 (gemm.cuh) and spare h the rounding to bf16. A pair's
+// CTAs hold half each.
+__host__ __device__ constexpr int token_rows(int nt, bool down)
+{
+    return nt >= kPairColumns ? nt / 2 : down && nt <= kSplitColumns ? 2 * nt : nt;
+}
+
 struct CtaLayout {
     uint32_t a, b, info, bars, bytes;
 };
 
 // Offsets from the first 1024-byte boundary of the CTA's shared memory.
-__host__ __device__ inline CtaLayout cta_layout(int nt, int stages)
+__host__ __device__ inline CtaLayout cta_layout(int nt, bool down, int stages)
 {
     CtaLayout L;
     uint32_t o = 0;
     L.a = o; o += static_cast<uint32_t>(stages) * kRows * kStepBytes;
-    L.b = o; o += static_cast<uint32_t>(stages) * (nt >= kPairColumns ? nt / 2 : nt) * kStepBytes;
+    L.b = o; o += static_cast<uint32_t>(stages) * token_rows(nt, down) * kStepBytes;
     L.info = o; o += static_cast<uint32_t>(nt) * 8;
     o = (o + 15) / 16 * 16;
     L.bars = o; o += sizeof(GemmBars);
@@ -134,14 +143,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 {
     extern __shared__ unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const CtaLayout L = cta_layout(NT, a.stages);
+    const CtaLayout L = cta_layout(NT, DOWN, a.stages);
     GemmBars& bars = *reinterpret_cast<GemmBars*>(smem + L.bars);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr bool kPair = NT >= kPairColumns;
     constexpr int kCtas = kPair ? 2 : 1;
     const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
-    constexpr uint32_t kColumns = 2 * NT;  // two accumulators: one fills while the other is read
-    constexpr uint32_t a_bytes = kRows * kStepBytes, b_bytes = NT / kCtas * kStepBytes;
+    constexpr bool kSplit = NT <= kSplitColumns;  // h in two parts
+    constexpr int kAcc = DOWN && kSplit ? 2 * NT : NT;
+    constexpr uint32_t kColumns = 2 * kAcc;  // two accumulators: one fills while the other is read
+    constexpr uint32_t a_bytes = kRows * kStepBytes, b_bytes = token_rows(NT, DOWN) * kStepBytes;
     const uint32_t ring_a = smem_addr(smem + L.a), ring_b = smem_addr(smem + L.b);
 
     if (warp == 1) tmem_alloc<kPair>(&bars.tmem, kColumns);
@@ -229,6 +240,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             // (a pair's CTAs bring half of the columns' tokens each)
             constexpr int kRound = 16 * kCtas;
             const int cols = max((n + kRound - 1) / kRound, 1) * kRound, boxes = (cols / kCtas + box - 1) / box;
+            constexpr int kParts = DOWN && kSplit ? 2 : 1;
             int4 row[kScattered ? NT / 4 : 1];
             if (kScattered) {
 #pragma unroll
@@ -245,8 +257,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (!ok) break;
                     uint64_t* full = &bars.full[pos.s];
                     const uint32_t dst = ring_b + pos.s * b_bytes;
-                    if (k == 0) bars.cols[pos.s] = cols;
-                    if (rank == 0) mbar_expect(full, (kScattered ? cols : boxes * box * kCtas) * kStepBytes);
+                    if (k == 0) bars.cols[pos.s] = cols * kParts;
+                    if (rank == 0) mbar_expect(full, (kScattered ? cols : boxes * box * kCtas * kParts) * kStepBytes);
                     ++issued;
                     if (!a.drop) {
                         if (kScattered) {
@@ -259,6 +271,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 const uint32_t to = dst + g * box * kStepBytes;
                                 if (kPair) load_box2_pair(to, &map_t, k * kStepK, first + g * box, cluster_addr(full, 0));
                                 else load_box2(to, &map_t, k * kStepK, first + g * box, full);
+                                if (kParts == 2) load_box2(to + cols * kStepBytes, &map_t, k * kStepK, a.cap + first + g * box, full);
                             }
                         }
                     }
@@ -281,7 +294,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 ok = seen < 2 || wait(&bars.acc_empty[buf], ((seen >> 1) - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = tmem + buf * NT;
+                const uint32_t d = tmem + buf * kAcc;
                 uint32_t desc = 0;
                 for (int k = 0; k < ksteps; ++k) {
                     ok = poll.take(wait, bars, pos, a.stages);
@@ -323,13 +336,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             if (!epilogue_wait(wait, &bars.acc_full[buf], (seen >> 1) & 1)) break;
             tc_fence_after();
-            const uint32_t acc = tmem + buf * NT + (static_cast<uint32_t>(q * 32) << 16);
+            const uint32_t acc = tmem + buf * kAcc + (static_cast<uint32_t>(q * 32) << 16);
             if (DOWN) {
                 const int row = m * kRows + et;
                 const bool mine = row < a.H;
                 for (int c0 = 0; c0 < n; c0 += 16) {
                     float v[16];
                     tmem_load16(acc + c0, v);
+                    if (kSplit) {
+                        float lo[16];
+                        tmem_load16(acc + ((n + 15) & ~15) + c0, lo);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) v[c] += lo[c];
+                    }
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
                         if (mine && c0 + c < n)
@@ -356,8 +375,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         for (int c = 0; c < 16; c += 2) {
                             const float other = __shfl_xor_sync(kFull, low ? v[c + 1] : v[c], 16);
                             const float g = low ? v[c] : other, w = low ? other : v[c + 1];
-                            if (mine && c0 + c + (low ? 0 : 1) < n)
-                                h[static_cast<long long>(c0 + c) * a.I] = __float2bfloat16_rn(act_f32(g, a.act) * w);
+                            if (mine && c0 + c + (low ? 0 : 1) < n) {
+                                const float f = act_f32(g, a.act) * w;
+                                const __nv_bfloat16 hi = __float2bfloat16_rn(f);
+                                h[static_cast<long long>(c0 + c) * a.I] = hi;
+                                const float r = f - __bfloat162float(hi);  // of an infinity: none
+                                if (kSplit)
+                                    h[(static_cast<long long>(a.cap) + c0 + c) * a.I] =
+                                        __float2bfloat16_rn(isinf(__bfloat162float(hi)) ? 0.0f : r);
+                            }
                         }
                     }
                 tc_fence_before();
@@ -400,18 +426,18 @@ namespace {
 constexpr int kSmemBudget = 200 * 1024;
 
 // As many stages as the budget holds.
-int stages_for(int nt)
+int stages_for(int nt, bool down)
 {
     int s = kMaxStages;
-    while (s > 2 && cta_layout(nt, s).bytes > kSmemBudget) --s;
+    while (s > 2 && cta_layout(nt, down, s).bytes > kSmemBudget) --s;
     return s;
 }
 
 template <int NT, bool DOWN>
 int launch_one(const CUtensorMap& map_w, const CUtensorMap& map_t, ExpertArgs a, long long units, cudaStream_t st)
 {
-    a.stages = stages_for(NT);
-    const size_t smem = cta_layout(NT, a.stages).bytes;
+    a.stages = stages_for(NT, DOWN);
+    const size_t smem = cta_layout(NT, DOWN, a.stages).bytes;
     const void* f = reinterpret_cast<const void*>(&k_experts<NT, DOWN>);
     const int e = ensure_smem(f, smem);
     if (e != cudaSuccess) return e;
