@@ -9,8 +9,8 @@
 namespace mr {
 
 // act(g) in fp32: SiLU g / (1 + exp(-g)), or GELU g * Phi(g). The hardware's
-// base-2 exponential and reciprocal are off by a few units of the last place,
-// far below the rounding of h to bf16 that follows.
+// base-2 exponential and reciprocal are off by a few units of the last place (the
+// exponential by |g| / 2 of them more), below the 16 bits that h keeps.
 __device__ __forceinline__ float act_f32(float g, int act)
 {
     if (act == MR_SILU) return __fdividef(g, 1.0f + exp2_hw(-g * kLog2e));

@@ -6,12 +6,12 @@
 //   k_experts_down  y[t][j] = weight * (w2[e] . h[p])
 //   k_experts_sum   out[t] = sum_j y[t][j], in slot order
 //
-// The first two are one persistent CTA per SM over units (block, row tile); see gemm.cuh
-// for the operands' roles. A unit of `up` holds 64 gate rows and the same 64 up
-// rows, alternating by 16, so that a warp of the epilogue has both
-// factors of h and one shuffle brings them together.
+// The first two are one persistent CTA per SM over units (block, row tile); see
+// gemm.cuh for the operands' roles. A unit of `up` holds 64 gate rows and the same
+// 64 up rows, alternating by 16, so that a warp of the epilogue has both factors
+// of h and one shuffle brings them together.
 //
-// Blocks of 64 pairs and more (prompts) read x from a copy in sorted order that
+// Blocks of 32 pairs and more read x from a copy in sorted order that
 // k_experts_gather makes: a copy of 4 scattered rows takes the tensor-copy
 // engine 80 clocks, of 64 consecutive rows 120, and each row tile of w13 reads
 // the block's rows again.

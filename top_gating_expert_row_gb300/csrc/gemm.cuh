@@ -16,8 +16,8 @@
 //
 // Prompts (tiles of 256 tokens): a pair of CTAs makes one product of 256 rows,
 // each holding 128 rows of the weights and half of the tokens (cta_group::2). A
-// k-step then brings an SM 32 KB instead of 48, and what an SM takes in, 64 to 70
-// bytes a clock, bounds such steps (48 KB: 389 ns a step of 280).
+// k-step then brings an SM 32 KB instead of 48 and the ring holds 6 steps instead
+// of 4 (T=8192 E=8 k=2 H=I=2048: `down` 114 -> 100 us, `up` 178 -> 176).
 #pragma once
 
 #include <cuda.h>
@@ -49,7 +49,8 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes)
 // One lane of a converged warp. Instructions of the tensor path take their
 // operands from uniform registers; under this predicate the compiler knows that
 // a single thread runs them, while `lane == 0` makes it loop over the lanes for
-// each (measured: 350 ns a k-step of four products instead of under 100).
+// each (T=1 E=256 k=8, with time stamps: 350 ns a k-step of four products, 256
+// under the predicate).
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t p;
