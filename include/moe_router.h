@@ -291,7 +291,8 @@ int moe_router_fused_fwd_sort(const mr_router_params* p, const void* logits, int
  * Activations and weights are bf16, products are accumulated in fp32. Any sizes and
  * any alignment of the element type are accepted: rows that are multiples of 16 bytes
  * at 16-byte aligned bases (H, I, K and rank multiples of 8) take the tensor-core
- * path, anything else a plain one (the same results to within rounding, slower).
+ * path, anything else a plain one (the same results to within rounding, slower). So
+ * do experts' calls of about 2^30 pairs and more, which the first counts in 32 bits.
  */
 typedef enum { MR_SILU = 0, MR_GELU = 1 } mr_act; /* GELU: x * Phi(x), with the error function */
 

@@ -228,7 +228,15 @@ int check_adapter(const mr_adapter_params* p)
 struct ExpertPlan {
     size_t idx, w, h, xs, sids, eids, npp, y, sort, sort_bytes, bytes;
     int nt, cap, mt_up, mt_down;
+    bool tensor;  // the sizes allow the tensor-core kernels (else cap and the parts beyond h are 0)
 };
+
+// Rows of the sorted layout and units that the tensor-core kernels count in 32
+// bits: a row index goes up by a grid's worth of warps past the last one, and is
+// doubled where h has two parts; a unit goes up by the grid. Larger calls take
+// the plain kernels, which count in 64.
+constexpr size_t kMaxRows = (size_t(1) << 30) - (1 << 16);
+constexpr long long kMaxUnits = INT_MAX - (1 << 16);
 
 size_t part(size_t& o, size_t bytes)
 {
@@ -261,26 +269,27 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     const size_t P = static_cast<size_t>(p.T) * p.topk;
     ExpertPlan w;
     w.nt = columns_for(static_cast<long long>(P), p.E);
-    // block sizes down to those whose padded total stays an int
-    while (w.nt > 16 && moe_sort_capacity(p.T, p.topk, p.E, w.nt) >= INT_MAX) w.nt /= 2;
     const size_t cap = moe_sort_capacity(p.T, p.topk, p.E, w.nt);
-    w.cap = cap < INT_MAX ? static_cast<int>(cap) : -1;
     w.mt_up = (p.I + 63) / 64;
     w.mt_down = (p.H + 127) / 128;
+    // whole 16-byte rows, an expert's weights below 2^40 bytes, counts of 32 bits
+    w.tensor = p.H % 8 == 0 && p.I % 8 == 0 && static_cast<long long>(p.I) * p.H < (1ll << 37) && cap <= kMaxRows &&
+               static_cast<long long>(cap / w.nt + 1) * std::max(w.mt_up, w.mt_down) <= kMaxUnits;
+    const size_t rows = w.tensor ? cap : 0;
+    w.cap = static_cast<int>(rows);
     size_t o = 0;
     w.idx = part(o, route ? P * 4 : 0);
     w.w = part(o, route ? P * 4 : 0);
-    w.sids = part(o, cap * 4);
-    w.eids = part(o, (cap / w.nt + 1) * 4);
-    w.npp = part(o, 4);
-    w.sort_bytes = moe_sort_workspace_bytes(p.T, p.topk, p.E, w.nt);
-    if (route) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
+    w.sids = part(o, rows * 4);
+    w.eids = part(o, w.tensor ? (rows / w.nt + 1) * 4 : 0);
+    w.npp = part(o, w.tensor ? 4 : 0);
+    w.sort_bytes = w.tensor ? moe_sort_workspace_bytes(p.T, p.topk, p.E, w.nt) : 0;
+    if (route && w.tensor) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
     w.sort = part(o, w.sort_bytes);
-    const bool whole = p.H % 8 == 0 && p.I % 8 == 0;  // else the plain kernels
     // few pairs: fp32; narrow blocks: two parts
-    w.h = part(o, (whole ? std::max(w.nt <= kSplitColumns ? 2 * cap : cap, 2 * P) : P) * p.I * 2);
-    w.xs = part(o, whole && w.nt >= kGatherColumns ? cap * p.H * 2 : 0);
-    w.y = part(o, whole ? P * p.H * 4 : 0);
+    w.h = part(o, (w.tensor ? std::max(w.nt <= kSplitColumns ? 2 * rows : rows, 2 * P) : P) * p.I * 2);
+    w.xs = part(o, w.nt >= kGatherColumns ? rows * p.H * 2 : 0);
+    w.y = part(o, w.tensor ? P * p.H * 4 : 0);
     w.bytes = o;
     return w;
 }
@@ -345,12 +354,10 @@ int launch_layer_few(const mr_router_params* p, const RouteArgs& r, const FewArg
 }
 
 // Whether the tensor-core kernels' copies can address these arrays: 16-byte
-// aligned bases and row strides, an expert's weights below 2^40 bytes.
-bool tensor_path(const mr_expert_params& p, const ExpertPlan& plan, const void* x, const void* w13, const void* w2)
+// aligned bases.
+bool tensor_path(const ExpertPlan& plan, const void* x, const void* w13, const void* w2)
 {
-    const long long blocks = plan.cap / plan.nt + 1;
-    return plan.cap > 0 && p.H % 8 == 0 && p.I % 8 == 0 && aligned(x, 16) && aligned(w13, 16) && aligned(w2, 16) &&
-           static_cast<long long>(p.I) * p.H < (1ll << 37) && blocks * std::max(plan.mt_up, plan.mt_down) < INT_MAX;
+    return plan.tensor && aligned(x, 16) && aligned(w13, 16) && aligned(w2, 16);
 }
 
 int experts_tensor(const mr_expert_params& p, const void* x, const int32_t* idx, const float* w, const void* w13,
@@ -465,7 +472,7 @@ AdapterPlan adapter_plan(const mr_adapter_params& p)
 bool adapter_tensor_path(const mr_adapter_params& p, const AdapterPlan& plan, const void* x, const void* w,
                          const void* a, const void* b)
 {
-    return p.K % 8 == 0 && aligned(x, 16) && aligned(w, 16) && static_cast<long long>(plan.tiles) * plan.mt < INT_MAX &&
+    return p.K % 8 == 0 && aligned(x, 16) && aligned(w, 16) && static_cast<long long>(plan.tiles) * plan.mt <= kMaxUnits &&
            (p.n_adapters == 0 || (p.rank % 8 == 0 && p.rank <= 128 && aligned(a, 16) && aligned(b, 16)));
 }
 
@@ -523,7 +530,7 @@ int moe_experts_fwd(const mr_expert_params* p, const void* x, const int32_t* top
         const int e = launch_experts_few<false>(a, st);
         return e != cudaSuccess ? MR_ECUDA : from_cuda(launch_experts_few<true>(a, st));
     }
-    if (!tensor_path(*p, plan, x, w13, w2))
+    if (!tensor_path(plan, x, w13, w2))
         return experts_plain(*p, x, topk_idx, topk_w, w13, w2, out, ws, plan, status, st);
     const int e = moe_sort(topk_idx, nullptr, p->T, p->topk, p->E, plan.nt, reinterpret_cast<int32_t*>(ws + plan.sids),
                            nullptr, reinterpret_cast<int32_t*>(ws + plan.eids),
@@ -569,7 +576,7 @@ int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* 
         const int e = launch_layer_few(p, r, a, false, st);
         return e != cudaSuccess ? MR_ECUDA : from_cuda(launch_layer_few(p, r, a, true, st));
     }
-    if (!tensor_path(q, plan, x, w13, w2)) {
+    if (!tensor_path(plan, x, w13, w2)) {
         rc = moe_router_fwd(p, logits, nullptr, nullptr, nullptr, idx, w, status, stream);
         return rc != MR_OK ? rc : experts_plain(q, x, idx, w, w13, w2, out, ws, plan, status, st);
     }
