@@ -1,0 +1,57 @@
+"""Edges of the experts' products, the layer and the adapter projection on the GPU: values far from the usual, the bits
+that intermediate values keep, sizes at which rings wrap and units follow one another."""
+import pytest
+import torch
+
+from test_gpu_layer import make_adapters, make_experts
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# ---- infinite weights ---------------------------------------------------------------------------------------------
+
+# a few pairs, narrow blocks (16, 32 and 64 pairs), blocks of 128 and 256, rows for the plain kernels
+INFINITE = [(1, 4, 2, 64, 32), (16, 64, 2, 128, 64), (40, 16, 2, 128, 64), (40, 8, 2, 128, 64), (100, 8, 2, 128, 64),
+            (700, 4, 2, 128, 64), (40, 8, 2, 33, 17)]
+
+
+@pytest.mark.parametrize("size", INFINITE, ids=lambda s: "T%d_E%d_k%d_H%d_I%d" % s)
+def test_an_infinite_weight_gives_an_infinity(mr, size):
+    """One infinite element of w2: h_i * inf + (finite) is an infinity of h_i's sign, on every path."""
+    x, idx, w, w13, w2 = make_experts(*size, seed=11)
+    T, E, k, H, I = size
+    e, row, i = int(idx[0, 0]), 3, 5
+    clean = mr.experts(*[t.cuda() for t in (x, idx, w, w13, w2)]).cpu()
+    w2[e, row, i] = float("inf")
+    got = mr.experts(*[t.cuda() for t in (x, idx, w, w13, w2)]).cpu()
+    gu = x.double() @ w13[e].double().t()
+    sign = torch.sign(gu[:, i] * gu[:, I + i])  # of h: SiLU has its argument's sign
+    hit = (idx == e).any(1)
+    assert (sign != 0).all()
+    want = clean.clone()
+    want[hit, row] = (sign[hit] * float("inf")).to(BF16)
+    assert torch.equal(got, want)
+
+
+# T, K, N, rank, adapters, out: one token, tiles of at most 64 tokens, wide tiles of one adapter, the plain kernels
+INFINITE_ADAPTERS = [(1, 64, 40, 8, 2, F32), (20, 256, 128, 16, 2, BF16), (300, 128, 72, 24, 2, F32),
+                     (20000, 64, 128, 64, 1, BF16), (40000, 64, 128, 40, 1, BF16), (20, 33, 17, 9, 2, F32)]
+
+
+@pytest.mark.parametrize("case", INFINITE_ADAPTERS, ids=lambda c: "T%d_K%d_N%d_r%d_n%d" % c[:5])
+def test_an_infinite_element_of_b_gives_an_infinity(mr, case):
+    *size, out = case
+    x, w, a, b, _, sc = make_adapters(*size, seed=12)
+    ad = torch.zeros(size[0], dtype=torch.int32)
+    clean = mr.adapter_proj(*[t.cuda() for t in (x, w, a, b, ad, sc)], out_dtype=out).cpu()
+    row, q = 5, 7
+    b[0, row, q] = float("inf")
+    got = mr.adapter_proj(*[t.cuda() for t in (x, w, a, b, ad, sc)], out_dtype=out).cpu()
+    low = x.double() @ a[0, q].double()
+    # a sum over K in fp32 has the sign of the exact one unless it is next to zero
+    sure = low.abs() > size[1] * 2.0 ** -23 * (x.double().abs() @ a[0, q].double().abs())
+    assert sure.double().mean() > 0.999
+    want = clean.clone()
+    want[:, row] = (torch.sign(low) * float("inf")).to(out)
+    assert torch.equal(got[sure], want[sure])

@@ -421,17 +421,17 @@ __device__ __forceinline__ void unpack8(uint4 p, float (&v)[8])
     }
 }
 
-// hi and lo of 8 consecutive ranks, packed; an infinity has no remainder.
+// hi and lo of 8 consecutive ranks, packed.
 __device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo)
 {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        h[i] = *reinterpret_cast<const uint32_t*>(&p);
-        const float x = __low2float(p), y = __high2float(p);
-        const __nv_bfloat162 r = __floats2bfloat162_rn(isinf(x) ? 0.0f : v[2 * i] - x, isinf(y) ? 0.0f : v[2 * i + 1] - y);
-        l[i] = *reinterpret_cast<const uint32_t*>(&r);
+        uint32_t h0, l0, h1, l1;
+        split_f32(v[2 * i], h0, l0);
+        split_f32(v[2 * i + 1], h1, l1);
+        h[i] = h0 | h1 << 16;
+        l[i] = l0 | l1 << 16;
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);

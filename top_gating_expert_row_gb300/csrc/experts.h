@@ -17,6 +17,26 @@ __device__ __forceinline__ float act_f32(float g, int act)
     return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
 }
 
+// v as hi + lo, two bf16 (their bits), to 16 significant bits: hi is v cut off, lo
+// the rest rounded; v that has no rest, or is an infinity, is halved instead. So
+// both parts have v's sign and neither is zero unless v is (or is below 2^-100):
+// an infinite weight times either is the same infinity, the one of w * v. (Of hi
+// rounded to nearest, which would spare one bit more, the rest has the other sign
+// half of the time, and inf - inf and inf * 0 are NaN. A tiny stand-in for a rest
+// of zero costs exact sums their last bit: the tensor cores cut off, they do not
+// round.)
+__device__ __forceinline__ void split_f32(float v, uint32_t& hi, uint32_t& lo)
+{
+    const uint32_t bits = __float_as_uint(v);
+    const float rest = v - __uint_as_float(bits & 0xffff0000u);  // exact; NaN for an infinity
+    if (fabsf(rest) > 0.0f) {
+        hi = bits >> 16;
+        lo = __bfloat16_as_ushort(__float2bfloat16_rn(rest));
+    } else {
+        hi = lo = __float_as_uint(0.5f * v) >> 16;
+    }
+}
+
 // Waits on copies in flight when a CTA gives up (attempts of about a microsecond).
 constexpr uint32_t kDrainTries = 1u << 14;
 

@@ -377,12 +377,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             const float g = low ? v[c] : other, w = low ? other : v[c + 1];
                             if (mine && c0 + c + (low ? 0 : 1) < n) {
                                 const float f = act_f32(g, a.act) * w;
-                                const __nv_bfloat16 hi = __float2bfloat16_rn(f);
-                                h[static_cast<long long>(c0 + c) * a.I] = hi;
-                                const float r = f - __bfloat162float(hi);  // of an infinity: none
-                                if (kSplit)
-                                    h[(static_cast<long long>(a.cap) + c0 + c) * a.I] =
-                                        __float2bfloat16_rn(isinf(__bfloat162float(hi)) ? 0.0f : r);
+                                __nv_bfloat16* to = h + static_cast<long long>(c0 + c) * a.I;
+                                if (kSplit) {
+                                    uint32_t hi, lo;
+                                    split_f32(f, hi, lo);
+                                    *to = __ushort_as_bfloat16(static_cast<unsigned short>(hi));
+                                    to[static_cast<long long>(a.cap) * a.I] = __ushort_as_bfloat16(static_cast<unsigned short>(lo));
+                                } else {
+                                    *to = __float2bfloat16_rn(f);
+                                }
                             }
                         }
                     }
