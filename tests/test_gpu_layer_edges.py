@@ -55,3 +55,33 @@ def test_an_infinite_element_of_b_gives_an_infinity(mr, case):
     want = clean.clone()
     want[:, row] = (torch.sign(low) * float("inf")).to(out)
     assert torch.equal(got[sure], want[sure])
+
+
+# ---- gates far below zero -----------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("size", [(1, 2, 1, 64, 40), (12, 4, 1, 64, 40), (90, 4, 2, 64, 40), (9, 3, 2, 33, 41)],
+                         ids=lambda s: "T%d_E%d_k%d_H%d_I%d" % s)
+def test_gelu_of_gates_below_zero(mr, size):
+    """g * Phi(g) for g in [-6, -2] to bf16's precision: 1 + erf(g / sqrt 2) would leave 10 bits at -4 and none at -6.
+
+    x picks one column of w13, so g and u are exact, and w2 is the identity, so out is h rounded to bf16 (half a step:
+    2^-8 relative) once, or twice in blocks of more than 64 pairs. h itself: erfc to 2^-20 and its argument to 2^-23,
+    which |g|^2 <= 36 times enters the value: 2^-17.5; two parts: 2^-16. In all below 2^-7 + 2^-13."""
+    T, E, k, H, I = size
+    x, idx, w, w13, w2 = make_experts(*size, seed=13)
+    x = torch.zeros_like(x)
+    x[:, 2] = 1
+    w13[:, :I, 2] = torch.linspace(-6, -2, I).to(BF16)
+    w13[:, I:, 2] = 1
+    n = min(H, I)
+    w2 = torch.zeros_like(w2)
+    w2[:, range(n), range(n)] = 1
+    idx = idx[:, :1].contiguous()
+    w = torch.ones_like(w[:, :1])
+    got = mr.experts(*[t.cuda() for t in (x, idx, w, w13, w2)], act=mr.MR_GELU).cpu().double()
+    g = w13[0, :n, 2].double()
+    want = (0.5 * g * torch.special.erfc(-g * 0.5 ** 0.5)).expand(T, n)
+    off = ((got[:, :n] - want) / want).abs().max().item()
+    assert off <= 2.0 ** -7 + 2.0 ** -13, off
+    assert not got[:, n:].any()

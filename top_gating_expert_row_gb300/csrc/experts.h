@@ -10,11 +10,14 @@ namespace mr {
 
 // act(g) in fp32: SiLU g / (1 + exp(-g)), or GELU g * Phi(g). The hardware's
 // base-2 exponential and reciprocal are off by a few units of the last place (the
-// exponential by |g| / 2 of them more), below the 16 bits that h keeps.
+// exponential by |g| / 2 of them more), below the 16 bits that h keeps. Phi(g) is
+// erfc(-g / sqrt 2) / 2, which keeps them for g below zero as well (1 + erf(g /
+// sqrt 2) cancels: 10 bits at -4, none below -5.5); the rounding of its argument
+// enters the value g^2 times, 2^-17 at g = -8.
 __device__ __forceinline__ float act_f32(float g, int act)
 {
     if (act == MR_SILU) return __fdividef(g, 1.0f + exp2_hw(-g * kLog2e));
-    return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
+    return 0.5f * g * erfcf(-g * 0.70710678118654752f);
 }
 
 // v as hi + lo, two bf16 (their bits), to 16 significant bits: hi is v cut off, lo
