@@ -316,8 +316,9 @@ typedef struct {
  *   for each token t and slot j with e = topk_idx[t][j] in [0, E):
  *     g = w13[e][0:I] x[t],  u = w13[e][I:2I] x[t],  h = act(g) * u
  *     out[t] = sum_j topk_w[t][j] * (w2[e] h_j)      (fp32, slots in ascending j)
- * h is kept to 16 significant bits or more, or rounded to bf16 where experts have more
- * than 16 pairs in the mean.
+ * h is kept to 16 significant bits or more, but rounded to bf16 on the tensor cores'
+ * path where the experts that have pairs have more than 16 in the mean (T*topk over
+ * min(T*topk, E)): two parts would cost the products of w2 twice the time there.
  * x [T x H], topk_idx int32 [T x topk], topk_w fp32 [T x topk], w13 [E x 2I x H] (gate
  * rows, then up rows), w2 [E x H x I], out [T x H]. out must not overlap an input.
  * Slots whose id is outside [0, E) contribute nothing (a token of such slots alone gets a

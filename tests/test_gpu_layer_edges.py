@@ -3,7 +3,8 @@ that intermediate values keep, sizes at which rings wrap and units follow one an
 import pytest
 import torch
 
-from test_gpu_layer import make_adapters, make_experts
+from layer_reference import assert_within
+from test_gpu_layer import make_adapters, make_experts, shifted
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -85,3 +86,62 @@ def test_gelu_of_gates_below_zero(mr, size):
     off = ((got[:, :n] - want) / want).abs().max().item()
     assert off <= 2.0 ** -7 + 2.0 ** -13, off
     assert not got[:, n:].any()
+
+
+# ---- the bits that intermediate values keep -------------------------------------------------------------------------
+
+
+def cancelling_experts(T, E, k, H, I, seed):
+    """h's values two and two almost alike (gate rows that differ by one bf16 step of one element, the same up rows),
+    and w2 takes their differences: about 2^-9 of the values. Eight elements of x, so that sums over H are short."""
+    x, idx, w, w13, w2 = make_experts(T, E, k, H, I, seed)
+    x[:, 8:] = 0
+    w13 = w13 * 2
+    n = min(I // 2, H)
+    gate, up = w13[:, :I], w13[:, I:]
+    gate[:, 1:2 * n:2] = gate[:, 0:2 * n:2]
+    up[:, 1:2 * n:2] = up[:, 0:2 * n:2]
+    first = gate[:, 1:2 * n:2, 0].contiguous()
+    gate[:, 1:2 * n:2, 0] = (first.view(torch.int16) + 1).view(BF16)
+    w2 = torch.zeros_like(w2)
+    w2[:, range(n), range(0, 2 * n, 2)] = 1
+    w2[:, range(n), range(1, 2 * n, 2)] = -1
+    return x, idx, w, w13, w2
+
+
+def experts_by_pair(x, idx, w, w13, w2, unit):
+    """In 64 bits (value, bound for h off by at most `unit` of itself, the value with h rounded to bf16)."""
+    x, w, w13, w2 = x.double(), w.double(), w13.double(), w2.double()
+    T, H = x.shape
+    I = w2.shape[2]
+    out, err, short = [torch.zeros(T, H, dtype=torch.float64) for _ in range(3)]
+    for t in range(T):
+        for j in range(idx.shape[1]):
+            e = int(idx[t, j])
+            gu, mag = w13[e] @ x[t], w13[e].abs() @ x[t].abs()
+            g, u = gu[:I], gu[I:]
+            d = 8 * 2.0 ** -23 * mag  # fp32 sums of eight products
+            h = g * torch.sigmoid(g) * u
+            dh = 1.13 * d[:I] * (u.abs() + d[I:]) + g.abs() * d[I:] + (2.0 ** -20 + unit) * h.abs()
+            out[t] += w[t, j] * (w2[e] @ h)
+            short[t] += w[t, j] * (w2[e] @ h.to(BF16).double())
+            # sums of a few values of |h| in fp32
+            err[t] += w[t, j] * (w2[e].abs() @ (dh + 8 * 2.0 ** -23 * h.abs()))
+    return out, err + 2.0 ** -8 * (out.abs() + err) + 1e-30, short
+
+
+# a few pairs; blocks of 16, 32 and 64 pairs; odd rows (plain kernels)
+@pytest.mark.parametrize("size", [(1, 4, 2, 64, 32), (20, 64, 1, 64, 32), (30, 8, 2, 64, 32), (60, 8, 2, 128, 64),
+                                  (3, 4, 2, 33, 18), (60, 8, 2, 65, 30)], ids=lambda s: "T%d_E%d_k%d_H%d_I%d" % s)
+def test_h_keeps_sixteen_bits(mr, size):
+    v = cancelling_experts(*size, seed=14)
+    got = mr.experts(*[t.cuda() for t in v])
+    want, bound, short = experts_by_pair(*v, unit=2.0 ** -16)
+    assert ((short - want).abs() > 2 * bound).any()  # eight bits are told from sixteen
+    assert_within(got, want, bound, "out")
+
+
+def test_h_keeps_sixteen_bits_at_unaligned_bases(mr):
+    v = cancelling_experts(5, 4, 2, 64, 32, seed=15)
+    want, bound, _ = experts_by_pair(*v, unit=2.0 ** -16)
+    assert_within(mr.experts(*[shifted(t.cuda(), 1) for t in v]), want, bound, "out")

@@ -46,21 +46,24 @@ bool encode_map(CUtensorMap* m, const void* base, long long width, long long hei
 // and no alignment beyond the element's. They serve rows that the tensor-core
 // kernels' 16-byte copies cannot address.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float bf(const __nv_bfloat16* p)
+__device__ __forceinline__ float value(const __nv_bfloat16* p)
 {
     return bf16_bits_to_f32(__ldcg(reinterpret_cast<const unsigned short*>(p)));
 }
 
-__device__ __forceinline__ float warp_dot(const __nv_bfloat16* a, const __nv_bfloat16* b, int n, int lane)
+__device__ __forceinline__ float value(const float* p) { return __ldcg(p); }
+
+template <typename B>
+__device__ __forceinline__ float warp_dot(const __nv_bfloat16* a, const B* b, int n, int lane)
 {
     float s = 0.0f;
-    for (int i = lane; i < n; i += 32) s = fmaf(bf(a + i), bf(b + i), s);
+    for (int i = lane; i < n; i += 32) s = fmaf(value(a + i), value(b + i), s);
     return warp_sum(s);
 }
 
 // h[pair][i] = act(w13[e][i] . x[t]) * (w13[e][I + i] . x[t]); pairs without an expert are left out
 __global__ void k_experts_up_plain(const __nv_bfloat16* x, const int32_t* idx, const __nv_bfloat16* w13,
-                                   __nv_bfloat16* h, long long P, int topk, int H, int I, int E, int act,
+                                   float* h, long long P, int topk, int H, int I, int E, int act,
                                    int32_t* status)
 {
     pdl_wait();
@@ -79,12 +82,12 @@ __global__ void k_experts_up_plain(const __nv_bfloat16* x, const int32_t* idx, c
         const __nv_bfloat16* w = w13 + (static_cast<long long>(e) * 2 * I + i) * H;
         const float g = warp_dot(w, row, H, lane);
         const float v = warp_dot(w + static_cast<long long>(I) * H, row, H, lane);
-        if (lane == 0) h[u] = __float2bfloat16_rn(act_f32(g, act) * v);
+        if (lane == 0) h[u] = act_f32(g, act) * v;
     }
 }
 
 // out[t][c] = sum_j weight[t][j] * (w2[e_j][c] . h[t][j])
-__global__ void k_experts_down_plain(const __nv_bfloat16* h, const int32_t* idx, const float* weight,
+__global__ void k_experts_down_plain(const float* h, const int32_t* idx, const float* weight,
                                      const __nv_bfloat16* w2, __nv_bfloat16* out, long long T, int topk, int H, int I,
                                      int E)
 {
@@ -144,7 +147,7 @@ __global__ void k_adapter_proj_plain(const __nv_bfloat16* x, const __nv_bfloat16
         if (ad >= 0 && ad < n_adapters) {
             const __nv_bfloat16* brow = b + (static_cast<long long>(ad) * N + c) * rank;
             float v = 0.0f;
-            for (int q = lane; q < rank; q += 32) v = fmaf(bf(brow + q), __ldcg(s + t * rank + q), v);
+            for (int q = lane; q < rank; q += 32) v = fmaf(value(brow + q), __ldcg(s + t * rank + q), v);
             acc += warp_sum(v);
         }
         if (lane == 0) store_scalar(out + u, acc);
@@ -286,8 +289,8 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
     w.sort_bytes = w.tensor ? moe_sort_workspace_bytes(p.T, p.topk, p.E, w.nt) : 0;
     if (route && w.tensor) w.sort_bytes = std::max(w.sort_bytes, moe_router_fused_workspace_bytes(route, w.nt));
     w.sort = part(o, w.sort_bytes);
-    // few pairs: fp32; narrow blocks: two parts
-    w.h = part(o, (w.tensor ? std::max(w.nt <= kSplitColumns ? 2 * rows : rows, 2 * P) : P) * p.I * 2);
+    // few pairs and plain kernels: fp32; narrow blocks: two parts
+    w.h = part(o, std::max(w.nt <= kSplitColumns ? 2 * rows : rows, 2 * P) * p.I * 2);
     w.xs = part(o, w.nt >= kGatherColumns ? rows * p.H * 2 : 0);
     w.y = part(o, w.tensor ? P * p.H * 4 : 0);
     w.bytes = o;
@@ -481,7 +484,7 @@ int experts_plain(const mr_expert_params& p, const void* x, const int32_t* idx, 
                   cudaStream_t st)
 {
     using B = __nv_bfloat16;
-    B* h = reinterpret_cast<B*>(ws + plan.h);
+    float* h = reinterpret_cast<float*>(ws + plan.h);
     const long long P = static_cast<long long>(p.T) * p.topk;
     int g = plain_grid(reinterpret_cast<const void*>(&k_experts_up_plain), P * p.I);
     if (g < 1) return MR_ECUDA;
@@ -491,7 +494,7 @@ int experts_plain(const mr_expert_params& p, const void* x, const int32_t* idx, 
     g = plain_grid(reinterpret_cast<const void*>(&k_experts_down_plain), static_cast<long long>(p.T) * p.H);
     if (g < 1) return MR_ECUDA;
     return from_cuda(launch_kernel(k_experts_down_plain, dim3(g), dim3(kPlainThreads), 0, st, 0,
-                                   static_cast<const B*>(h), idx, w, static_cast<const B*>(w2), static_cast<B*>(out),
+                                   static_cast<const float*>(h), idx, w, static_cast<const B*>(w2), static_cast<B*>(out),
                                    static_cast<long long>(p.T), p.topk, p.H, p.I, p.E));
 }
 
