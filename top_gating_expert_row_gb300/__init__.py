@@ -507,6 +507,13 @@ def aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor, T: in
 
 
 # ------------------------------------------------------------------- the layer behind the router
+# Serving operators: they have no backward pass, so inputs that ask for a gradient are refused instead of giving
+# results that are cut off from them (under torch.no_grad(), as in serving, they are taken).
+
+
+def _forward_only(*tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError("this operator has no backward pass: call it under torch.no_grad(), or detach its inputs")
 
 
 def _check(what: str, t: torch.Tensor, shape, dtype, device) -> None:
@@ -622,7 +629,8 @@ def experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, w13: 
             act: int = MR_SILU, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_experts_fwd with a freshly allocated output and workspace: out [T, H] (bf16) of x [T, H] (bf16) through
     the experts topk_idx [T, topk] (int32; ids outside [0, E) are skipped) with weights topk_w (fp32).
-    w13 [E, 2*I, H] holds each expert's gate rows, then its up rows; w2 is [E, H, I]."""
+    w13 [E, 2*I, H] holds each expert's gate rows, then its up rows; w2 is [E, H, I]. No backward pass."""
+    _forward_only(x, topk_w, w13, w2)
     E, H, I = _weights_shape(x, w13, w2)
     if topk_idx.dim() != 2:
         raise ValueError("topk_idx is [T, topk]")
@@ -645,7 +653,8 @@ def layer(x: torch.Tensor, logits: torch.Tensor, topk: int, w13: torch.Tensor, w
           bias: Optional[torch.Tensor] = None) -> dict:
     """moe_layer_fwd with freshly allocated outputs: the layer's out [T, H] and the routing it took (topk_idx,
     topk_w) from x [T, H] (bf16) and router logits [T, E] (fp32 or bf16). Routing options as for route(); w13 / w2
-    as for experts(), with the shared experts last."""
+    as for experts(), with the shared experts last. No backward pass."""
+    _forward_only(x, logits, w13, w2, bias)
     E_tot, H, I = _weights_shape(x, w13, w2)
     T, E, dev = x.shape[0], E_tot - n_shared, x.device
     dtype = _dtype_code(logits)
@@ -675,7 +684,9 @@ def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = N
                  status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_adapter_proj_fwd with a freshly allocated output: x [T, K] through the shared w [N, K], plus for each
     token its adapter's scale[i] * b[i] (a[i] x), i = adapter[t] (int32 [T]; negative: none), a [n, rank, K],
-    b [n, N, rank]; out [T, N] in out_dtype (bf16 or fp32). Without a, b, adapter: the projection alone."""
+    b [n, N, rank]; out [T, N] in out_dtype (bf16 or fp32). Without a, b, adapter: the projection alone. No backward
+    pass."""
+    _forward_only(x, w, a, b, scale)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x is [T, K], w [N, K]")
     (T, K), N, dev = x.shape, w.shape[0], x.device
