@@ -3,7 +3,7 @@ that intermediate values keep, sizes at which rings wrap and units follow one an
 import pytest
 import torch
 
-from layer_reference import assert_within
+from layer_reference import assert_within, experts64
 from test_gpu_layer import make_adapters, make_experts, shifted
 
 pytestmark = pytest.mark.gpu
@@ -145,3 +145,105 @@ def test_h_keeps_sixteen_bits_at_unaligned_bases(mr):
     v = cancelling_experts(5, 4, 2, 64, 32, seed=15)
     want, bound, _ = experts_by_pair(*v, unit=2.0 ** -16)
     assert_within(mr.experts(*[shifted(t.cuda(), 1) for t in v]), want, bound, "out")
+
+
+@pytest.mark.parametrize("T", [8, 32, 100])
+def test_fp32_projection_of_4096(mr, T):
+    """The tensor cores' sum loses last bits: 2e-6 of the output's norm when it runs over all of K = 4096 and 1.5e-6
+    over parts of 512, against 0.9e-6 with the parts of 256 that fp32 outputs take."""
+    x, w, *_ = make_adapters(T, 4096, 512, 8, 1, seed=16)
+    want = x.double() @ w.double().t()
+    got = mr.adapter_proj(x.cuda(), w.cuda(), out_dtype=F32).cpu().double()
+    assert ((got - want).norm() / want.norm()).item() <= 1.2e-6
+
+
+# ---- rings that wrap, accumulators handed back, units one after another -----------------------------------------------
+
+
+# pairs of CTAs with 16 and more steps of K a unit and several units a pair, the last row tile without a second one;
+# single CTAs with as many
+@pytest.mark.parametrize("size", [(6000, 4, 2, 2048, 1024), (5000, 3, 2, 1096, 1160), (3000, 40, 2, 1536, 1024),
+                                  (800, 60, 4, 1024, 1024), (48, 200, 8, 1032, 1160)],
+                         ids=lambda s: "T%d_E%d_k%d_H%d_I%d" % s)
+def test_experts_of_real_sizes(mr, size):
+    """Against the definition in 64 bits, by the norm of each token's row: rounding the output and h to bf16
+    (2^-8 at most, 2^-8 / sqrt 3 in the mean, each) stays below 2^-8 over a row of a thousand; a lost or stale step of
+    K is a tenth or more."""
+    T, E, k, H, I = size
+    x, idx, w, w13, w2 = [t.cuda() for t in make_experts(*size, seed=17)]
+    want = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        if len(t):
+            gu = x[t].double() @ w13[e].double().t()
+            h = gu[:, :I] * torch.sigmoid(gu[:, :I]) * gu[:, I:]
+            want.index_add_(0, t, (h @ w2[e].double().t()) * w[t, j, None].double())
+    first = mr.experts(x, idx, w, w13, w2)
+    off = (first.double() - want).norm(dim=1) / want.norm(dim=1)
+    assert off.max().item() <= 2.0 ** -8
+    for _ in range(3):
+        assert torch.equal(mr.experts(x, idx, w, w13, w2), first)
+
+
+def whole_adapters(T, K, N, r, n, segment, seed=18):
+    """Small whole numbers: every sum is exact in fp32, and the rank-space values fit 16 bits."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def rand(top, *shape):
+        return torch.randint(-top, top + 1, shape, generator=g, device="cuda").to(BF16)
+
+    x, w, a, b = rand(2, T, K), rand(2, N, K), rand(1, n, r, K), rand(1, n, N, r)
+    scale = 2.0 ** torch.randint(-1, 2, (n,), generator=g, device="cuda").float()
+    ad = torch.randint(-1, n, (-(-T // segment),), generator=g, device="cuda", dtype=torch.int32)
+    ad[0] = n - 1
+    ad = ad.repeat_interleave(segment)[:T].contiguous()
+    want = x.double() @ w.double().t()
+    for i in range(n):
+        t = (ad == i).nonzero()[:, 0]
+        low = x[t].double() @ a[i].double().t() * scale[i].double()
+        assert not len(t) or low.abs().max().item() < 2 ** 15  # halves among them
+        want[t] += low @ b[i].double().t()
+    assert want.abs().max().item() < 2 ** 22
+    return (x, w, a, b, ad, scale), want
+
+
+WHOLE = [
+    # T, K, N, rank, adapters, segment, out
+    # wide tiles (256 and 128 tokens) with many steps of K and several slices of the rank-space values: one adapter a
+    # tile, requests that end inside tiles, one a token
+    (4096, 1024, 4096, 64, 8, 512, BF16), (4096, 1024, 4096, 64, 8, 300, BF16), (4096, 1096, 4100, 128, 5, 4096, BF16),
+    (2048, 1544, 1536, 40, 6, 500, BF16), (2000, 1024, 1536, 64, 30, 1, BF16), (4096, 2048, 2304, 8, 3, 256, BF16),
+    # rank-space values on the tensor cores in tiles of 16, 32 and 64 tokens
+    (16, 40960, 256, 128, 3, 1, F32), (32, 20480, 200, 128, 40, 1, F32), (64, 8200, 256, 128, 64, 1, BF16),
+    (700, 2048, 512, 64, 9, 100, F32), (3600, 1104, 512, 32, 16, 29, F32), (3600, 1104, 256, 32, 4, 600, F32),
+    # a K for each CTA of a cluster, and units one after another without one
+    (40, 4096, 1024, 16, 40, 1, F32), (64, 1024, 20000, 16, 5, 7, F32), (2500, 520, 2048, 24, 6, 111, F32),
+]
+
+
+@pytest.mark.parametrize("case", WHOLE, ids=lambda c: "T%d_K%d_N%d_r%d_n%d_s%d" % c[:6])
+def test_adapter_sums_of_whole_numbers_are_exact(mr, case):
+    *size, out = case
+    v, want = whole_adapters(*size)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    first = mr.adapter_proj(*v, out_dtype=out, status=status)
+    assert torch.equal(first, want.to(out))
+    assert int(status.item()) == 0
+    for _ in range(3):
+        assert torch.equal(mr.adapter_proj(*v, out_dtype=out), first)
+
+
+def test_layer_with_bias_and_groups_against_the_oracle(mr, orc):
+    T, E, k, H, I = 50, 64, 9, 128, 64
+    x, _, _, w13, w2 = make_experts(T, E, k, H, I, seed=19, E_tot=E + 1)
+    g = torch.Generator().manual_seed(20)
+    logits, bias = torch.randn(T, E, generator=g), torch.rand(E, generator=g) - 0.5
+    for opts in (dict(n_shared=1, renorm=1, scaling=2.5), dict(n_shared=1, n_group=8, topk_group=4, renorm=1)):
+        got = mr.layer(x.cuda(), logits.cuda(), k, w13.cuda(), w2.cuda(), score_fn=mr.MR_SIGMOID, bias=bias.cuda(), **opts)
+        ref = orc.router_fwd(logits.numpy(), k, 1, 1, opts.get("n_group", 0), opts.get("topk_group", 0), 1,
+                             opts.get("scaling", 1.0), 1.0, bias.numpy())
+        assert torch.equal(got["topk_idx"].cpu(), torch.from_numpy(ref["topk_idx"]).to(torch.int32))
+        weights = torch.from_numpy(ref["topk_w"])
+        assert torch.allclose(got["topk_w"].cpu().double(), weights.double(), rtol=1e-6, atol=1e-7)
+        want, bound = experts64(x, got["topk_idx"].cpu(), got["topk_w"].cpu(), w13, w2)
+        assert_within(got["out"], want, bound, "out")
