@@ -161,9 +161,9 @@ def test_fp32_projection_of_4096(mr, T):
 
 
 # pairs of CTAs with 16 and more steps of K a unit and several units a pair, the last row tile without a second one;
-# single CTAs with as many
+# single CTAs with as many; one token below and above what the CUDA cores take
 @pytest.mark.parametrize("size", [(6000, 4, 2, 2048, 1024), (5000, 3, 2, 1096, 1160), (3000, 40, 2, 1536, 1024),
-                                  (800, 60, 4, 1024, 1024), (48, 200, 8, 1032, 1160)],
+                                  (800, 60, 4, 1024, 1024), (48, 200, 8, 1032, 1160), (1, 32, 8, 2048, 1024), (1, 8, 4, 2560, 2048)],
                          ids=lambda s: "T%d_E%d_k%d_H%d_I%d" % s)
 def test_experts_of_real_sizes(mr, size):
     """Against the definition in 64 bits, by the norm of each token's row: rounding the output and h to bf16

@@ -304,8 +304,8 @@ __global__ void __launch_bounds__(256) k_adapter_low_rows(const __nv_bfloat16* x
 // why). The row's product, and the loads of b's row, come before the rank-space
 // values are needed; the lanes share out the ranks. FUSED (one token): every CTA
 // makes the rank-space values itself, at most 64 KB of a from L2: a launch less
-// for the host, which costs an eager call 4.5 us, and up to 1.2 us more on the
-// GPU (5.0 against 3.8 at K=2048 N=256, 5.6 against 5.9 at K=N=2048).
+// for the host, which costs an eager call 3.3 us, and up to 2.2 us more on the GPU
+// (kFusedLowProducts, in experts.cu, has the figures).
 __host__ __device__ constexpr int few_threads(bool fused) { return fused ? 512 : 256; }
 
 template <int TOKENS, bool FUSED, typename OutT>

@@ -298,12 +298,15 @@ ExpertPlan expert_plan(const mr_expert_params& p, const mr_router_params* route)
 }
 
 // Few pairs: each pair's weights are read by itself, as fast as the tensor cores'
-// path reads them up to about 75 MB and without its 5 us of set-up: T=1 k=8
-// H=2048 I=768 22.0 us against 24.7, T=1 k=4 H=2048 I=1024 16.1 against 20.8, T=4
-// k=2 H=512 I=256 8.0 against 11.9; but T=2 k=8 H=2048 I=768 39 against 38, T=1
-// k=4 H=2560 I=2048 36 against 31.
+// path reads them up to about 100 MB and without its 5 us of set-up. Layers in a
+// CUDA graph, this path against that one, us: at 8.4M products 17.8 / 22.2 (T=1 k=8
+// H=2048), 16.4 / 20.8 (T=2 k=4 H=2048); at 12.6M 22.2 / 24.8, 21.4 / 23.4; at 16.8M
+// 25.9 / 27.9, 25.1 / 26.8, 25.6 / 26.5 (T=4 k=4 H=1024), 23.1 / 22.9 (T=8 k=4
+// H=512); at 15.7M 27.8 / 27.5 (T=1 k=4 H=2560); at 21.0M, past the border, 34.0 /
+// 31.1 there, but 31.1 / 35.3 (T=1 k=8 H=2048). Eager calls save the host two launches
+// (26 / 33) as long as that bounds them, up to about 17M.
 constexpr int kFewPairs = 32, kFewTokens = 8;
-constexpr long long kFewProducts = 13000000;  // P * H * I
+constexpr long long kFewProducts = 17000000;  // P * H * I
 constexpr size_t kFewSmem = 64 * 1024;
 
 bool few_path(const mr_expert_params& p, const void* x, const void* w13, const void* w2)
@@ -423,7 +426,12 @@ constexpr double kLowRowsProducts = 64 << 20;
 // 11.5 against 8.6 at N=4096; T=2 K=N=2048: 6.7 against 7.5).
 constexpr int kFewProjTokens = 4;
 constexpr long long kFewProjProducts = 10000000;
-// Rank-space values that every CTA of it makes for itself (one token), up to this many products.
+// Rank-space values that every CTA of it makes for itself (one token), up to this
+// many products: a launch less saves an eager call's host 3.3 us at any of them
+// (18.4 / 21.7), and what the GPU takes more stays below that: at 32K products 5.0 /
+// 3.9 (K=2048 N=256), 7.2 / 5.0 (K=4096 N=256), 7.4 / 6.6 (K=4096 N=1024), 5.6 / 6.0
+// (K=N=2048); at 48K, past the border, 7.0 / 3.9 (K=2048 N=256), at 64K 7.3 / 4.9
+// (K=4096 N=256), 7.7 / 4.8 (K=N=2048). (CUDA graph, us, made by each CTA / by a launch.)
 constexpr long long kFusedLowProducts = 32 << 10;
 
 AdapterPlan adapter_plan(const mr_adapter_params& p)
