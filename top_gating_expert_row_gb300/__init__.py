@@ -512,8 +512,9 @@ def aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor, T: in
 
 
 def _forward_only(*tensors) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError("this operator has no backward pass: call it under torch.no_grad(), or detach its inputs")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("this operator has no backward pass: call it under torch.no_grad(), or detach its inputs")
 
 
 def _check(what: str, t: torch.Tensor, shape, dtype, device) -> None:
