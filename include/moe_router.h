@@ -291,8 +291,10 @@ int moe_router_fused_fwd_sort(const mr_router_params* p, const void* logits, int
  * Activations and weights are bf16, products are accumulated in fp32. Any sizes and
  * any alignment of the element type are accepted: rows that are multiples of 16 bytes
  * at 16-byte aligned bases (H, I, K and rank multiples of 8) take the tensor-core
- * path, anything else a plain one (the same results to within rounding, slower). So
- * do experts' calls of about 2^30 pairs and more, which the first counts in 32 bits.
+ * path, anything else a plain one: the same results to within rounding, but a warp per
+ * output element, tens of times slower with many tokens. So do adapters of a rank above
+ * 128, and experts' calls of about 2^30 pairs and more, which the first counts in 32
+ * bits.
  */
 typedef enum { MR_SILU = 0, MR_GELU = 1 } mr_act; /* GELU: x * Phi(x), with the error function */
 
@@ -318,7 +320,7 @@ typedef struct {
  *     out[t] = sum_j topk_w[t][j] * (w2[e] h_j)      (fp32, slots in ascending j)
  * h is kept to 16 significant bits or more, but rounded to bf16 on the tensor cores'
  * path where the experts that have pairs have more than 16 in the mean (T*topk over
- * min(T*topk, E)): two parts would cost the products of w2 twice the time there.
+ * min(T*topk, E)): more would cost prompts up to half of their time again.
  * x [T x H], topk_idx int32 [T x topk], topk_w fp32 [T x topk], w13 [E x 2I x H] (gate
  * rows, then up rows), w2 [E x H x I], out [T x H]. out must not overlap an input.
  * Slots whose id is outside [0, E) contribute nothing (a token of such slots alone gets a
@@ -361,7 +363,8 @@ int moe_layer_fwd(const mr_router_params* p, int H, int I, int act, const void* 
  * Smaller ranks share a call by padding a's rows or b's columns with zeros. The rank-
  * space values are kept to 16 significant bits, sums in fp32. adapter[t] >= n_adapters
  * counts as none and raises *status to MR_ERANGE. n_adapters 0: no adapters (a, b,
- * scale, adapter ignored). out must not overlap an input.
+ * scale, adapter ignored). out must not overlap an input. Prompts in bf16 are fastest
+ * where aligned runs of 128 or 256 tokens name one adapter.
  * Limits: K, N, rank 1..MR_MAX_WIDTH, n_adapters >= 0. Workspace, status and errors as above.
  */
 typedef struct {

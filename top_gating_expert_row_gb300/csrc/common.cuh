@@ -281,11 +281,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch. Every kernel of the library may call
 // pdl_trigger on entry (the next kernel in the stream may be launched now and
-// run its own entry while this one works) and calls pdl_wait before its first
-// access to global memory (it returns once the previous kernel in the stream
-// has completed and its writes are visible; at once for a kernel launched
+// run its own entry while this one works) and calls pdl_wait before it reads what
+// its predecessor in the stream made or writes global memory (it returns once that
+// kernel has completed and its writes are visible; at once for a kernel launched
 // without the overlap). Since every kernel waits for its predecessor, each also
-// completes after all the kernels before it.
+// completes after all the kernels before it. Most wait before any access to global
+// memory. A kernel may read earlier only what was complete before its predecessor
+// passed pdl_wait, and only behind a predecessor that triggers after that: the
+// second kernels of the layer and of the adapter projection read weights, x and
+// the choice of experts so (k_experts<down>, k_layer_few<down>, k_experts_few<down>,
+// k_adapter_few, k_adapter_proj).
 // ---------------------------------------------------------------------------
 // Under the overlap a kernel runs while its predecessor is still writing, so
 // nothing that kernel produced may be read through the non-coherent read-only

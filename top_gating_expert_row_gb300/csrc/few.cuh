@@ -1,8 +1,11 @@
 // The layer for a few pairs (decode of one to a few tokens), on the CUDA cores
 // and without a sort: two launches, a warp per row of the weights.
 //
-//   k_few_up    h[p][i] = act(w13[e][i] . x_t) * (w13[e][I + i] . x_t)
-//   k_few_down  out[t][c] = sum_j weight[t][j] * (w2[e_j][c] . h[t][j])
+//   up    h[p][i] = act(w13[e][i] . x_t) * (w13[e][I + i] . x_t)
+//   down  out[t][c] = sum_j weight[t][j] * (w2[e_j][c] . h[t][j])
+//
+// k_experts_few (experts.cu) is either for a given choice of experts, k_layer_few
+// (layer_few.cu) with the routing.
 //
 // A pair's product is a matrix-vector one: each weight is used once, two
 // operations a weight, so the time is that of streaming the weights, and what
