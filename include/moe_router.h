@@ -375,6 +375,87 @@ int moe_adapter_proj_fwd(const mr_adapter_params* p, const void* x, const void* 
                          const int32_t* adapter, const float* scale, void* out, void* workspace,
                          size_t ws_bytes, int32_t* status, mr_stream_t stream);
 
+/*
+ * ---- Rows by expert and back, for training and serving: permutation, activation, weighted sum, dropout ----
+ *
+ * What a layer does around its experts' matrix products, each step with its gradient as a call of its own:
+ *   moe_sort -> moe_permute_fwd -> (product) -> moe_expert_act_fwd -> (product) -> moe_combine_fwd
+ *   moe_combine_bwd -> (products) -> moe_expert_act_bwd -> (products) -> moe_permute_bwd
+ * Rows are those of moe_sort's layout: n_rows of them have room (at least *num_tokens_post_pad; moe_sort_capacity()
+ * is always enough), the first *num_tokens_post_pad are in use, padding rows among them included; rows behind those
+ * are neither read nor written. x, rows, gradients and residuals share one dtype, MR_F32 or MR_BF16; sums are taken in
+ * fp32 in a fixed order and rounded once. H and I: 1..MR_MAX_WIDTH, any alignment of the element type; rows of a
+ * multiple of 8 elements at 16-byte (fp32: 32-byte) aligned bases are fastest. No workspace, no allocation.
+ * Outputs must not overlap inputs, except that out may be residual itself and dropout may work in place.
+ *
+ * Dropout. drop_p in [0, 1]; rng: two 64-bit words {seed, offset} in device memory, 8-byte aligned, read when the
+ * kernel runs (so a captured graph drops other elements after the caller advanced them); may be NULL where drop_p * 2^16
+ * rounds to 0. No mask is stored: element (row, col) is dropped iff its 16 random bits are below cut = drop_p * 2^16
+ * (rounded), otherwise it is multiplied by 2^16 / (2^16 - cut). The bits are word (col % 8) / 2 of Philox 4x32 with ten
+ * rounds, low half for even columns, under the key seed and the counter (col / 8, row, offset), low words first. A
+ * backward call with the same words drops the same elements. Calls that share a seed and an offset share their masks:
+ * give each step and layer offsets of its own. A dropped element is 0 whatever it held.
+ */
+typedef struct {
+    int32_t T, H, topk, n_rows, dtype;
+} mr_rows_params;
+
+/*
+ * moe_permute_fwd -- rows[r] = x[sorted_token_ids[r] / topk] for the rows in use, 0 at padding rows (any id outside
+ * [0, T*topk)); pair_row [T x topk] (int32): the row of each pair, -1 where topk_idx is outside [0, E_tot) (the pairs
+ * that moe_sort drops). topk_idx, sorted_token_ids (n_rows entries) and num_tokens_post_pad are moe_sort's.
+ * *status is raised to MR_ERANGE where num_tokens_post_pad exceeds n_rows (the rows behind are left out) or an id is
+ * outside [0, T*topk].
+ * moe_permute_bwd -- grad_x[t] = sum_j grad_rows[pair_row[t][j]], pairs of -1 left out.
+ * Errors: MR_EINVAL (null or misaligned pointer, T < 0, H, topk or E_tot < 1, n_rows < 0, unknown dtype, T*topk >=
+ * INT_MAX), MR_EUNSUPPORTED (H), MR_ECUDA. In this and the calls below a pair_row outside [-1, n_rows) counts as -1 and
+ * raises *status (nullable) to MR_ERANGE. T == 0 is a no-op.
+ */
+int moe_permute_fwd(const mr_rows_params* p, int E_tot, const void* x, const int32_t* topk_idx,
+                    const int32_t* sorted_token_ids, const int32_t* num_tokens_post_pad, void* rows, int32_t* pair_row,
+                    int32_t* status, mr_stream_t stream);
+int moe_permute_bwd(const mr_rows_params* p, const void* grad_rows, const int32_t* pair_row, void* grad_x,
+                    int32_t* status, mr_stream_t stream);
+
+/*
+ * moe_combine_fwd -- out[t] = residual[t] + dropout(sum_j topk_w[t][j] * rows[pair_row[t][j]]) over the pairs that have
+ * a row, in slot order; residual is nullable; dropout's row is t. A token without any such pair gives its residual, or 0.
+ * moe_combine_bwd -- with g[t] = grad_out[t] where kept, scaled (the residual's gradient is grad_out itself):
+ *   grad_rows[pair_row[t][j]] = topk_w[t][j] * g[t], 0 at padding rows;  grad_w[t][j] = <g[t], rows[pair_row[t][j]]>, 0
+ *   for pairs without a row. sorted_token_ids and num_tokens_post_pad say which rows are padding.
+ * Errors as above, and MR_EINVAL for a drop_p outside [0, 1] or without the rng it needs.
+ */
+int moe_combine_fwd(const mr_rows_params* p, const void* rows, const int32_t* pair_row, const float* topk_w,
+                    const void* residual, float drop_p, const void* rng, void* out, int32_t* status, mr_stream_t stream);
+int moe_combine_bwd(const mr_rows_params* p, const void* grad_out, const void* rows, const int32_t* pair_row,
+                    const float* topk_w, const int32_t* sorted_token_ids, const int32_t* num_tokens_post_pad,
+                    float drop_p, const void* rng, void* grad_rows, float* grad_w, int32_t* status, mr_stream_t stream);
+
+/*
+ * moe_expert_act_fwd -- h[r] = dropout(act(g) * u) for gu [n_rows x 2*I], a row's I gate values, then its I up values
+ * (the rows' product with w13); h [n_rows x I]; act: MR_SILU or MR_GELU. num_rows: nullable device int32, the rows in
+ * use (moe_sort's num_tokens_post_pad); NULL: all n_rows. Dropout's row is r.
+ * moe_expert_act_bwd -- d = grad_h where kept, scaled: grad_gu[r] = (d * u * act'(g), d * act(g)); h (nullable): h[r]
+ * computed again, for the gradient of w2. The activation is computed from gu, nothing else is kept of the forward.
+ * Errors as above. n_rows == 0 is a no-op.
+ */
+typedef struct {
+    int32_t n_rows, I, act, dtype;
+} mr_act_params;
+int moe_expert_act_fwd(const mr_act_params* p, const void* gu, const int32_t* num_rows, float drop_p, const void* rng,
+                       void* h, mr_stream_t stream);
+int moe_expert_act_bwd(const mr_act_params* p, const void* grad_h, const void* gu, const int32_t* num_rows, float drop_p,
+                       const void* rng, void* grad_gu, void* h, mr_stream_t stream);
+
+/*
+ * moe_dropout_fwd -- y[t] = residual[t] + dropout(x[t]) for x [T x H], e.g. hidden states before the router; residual is
+ * nullable. moe_dropout_bwd -- grad_x[t] = grad_y[t] where kept, scaled. Errors as above.
+ */
+int moe_dropout_fwd(int T, int H, int dtype, const void* x, const void* residual, float drop_p, const void* rng, void* y,
+                    mr_stream_t stream);
+int moe_dropout_bwd(int T, int H, int dtype, const void* grad_y, float drop_p, const void* rng, void* grad_x,
+                    mr_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* moe_router_strerror(int code);
 

@@ -50,12 +50,23 @@ class mr_adapter_params(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "n_adapters", "rank", "dtype", "out_dtype")]
 
 
+class mr_rows_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "topk", "n_rows", "dtype")]
+
+
+class mr_act_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_rows", "I", "act", "dtype")]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
 _PP = ctypes.POINTER(mr_router_params)
 _PE = ctypes.POINTER(mr_expert_params)
 _PA = ctypes.POINTER(mr_adapter_params)
+_PR = ctypes.POINTER(mr_rows_params)
+_PH = ctypes.POINTER(mr_act_params)
+_F = ctypes.c_float
 _SIGS = {
     "moe_router_fwd": ([_PP, _P, _P, _P, _P, _P, _P, _P, _P], _I),
     "moe_router_bwd": ([_PP, _P, _P, _P, _P, _P], _I),
@@ -76,6 +87,14 @@ _SIGS = {
     "moe_layer_fwd": ([_PP, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I),
     "moe_adapter_proj_workspace_bytes": ([_PA], _SZ),
     "moe_adapter_proj_fwd": ([_PA, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P], _I),
+    "moe_permute_fwd": ([_PR, _I, _P, _P, _P, _P, _P, _P, _P, _P], _I),
+    "moe_permute_bwd": ([_PR, _P, _P, _P, _P, _P], _I),
+    "moe_combine_fwd": ([_PR, _P, _P, _P, _P, _F, _P, _P, _P, _P], _I),
+    "moe_combine_bwd": ([_PR, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _P, _P], _I),
+    "moe_expert_act_fwd": ([_PH, _P, _P, _F, _P, _P, _P], _I),
+    "moe_expert_act_bwd": ([_PH, _P, _P, _P, _F, _P, _P, _P, _P], _I),
+    "moe_dropout_fwd": ([_I, _I, _I, _P, _P, _F, _P, _P, _P], _I),
+    "moe_dropout_bwd": ([_I, _I, _I, _P, _F, _P, _P, _P], _I),
     "moe_router_strerror": ([_I], ctypes.c_char_p),
     "moe_router_set_topk_path": ([_I, _I], _I),
     "moe_router_expf": ([_P, _P, _I, _P], _I),
@@ -366,6 +385,51 @@ def moe_adapter_proj_fwd(p: mr_adapter_params, x, w, a, b, adapter, scale, out, 
     return _ok(_lib.moe_adapter_proj_fwd(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(a), _ptr(b), _ptr(adapter),
                                          _ptr(scale), _ptr(out), _ptr(workspace), ws_bytes, _ptr(status),
                                          _stream(stream)), "moe_adapter_proj_fwd")
+
+
+def moe_permute_fwd(p: mr_rows_params, E_tot, x, topk_idx, sorted_token_ids, num_tokens_post_pad, rows, pair_row,
+                    status=None, stream=None) -> int:
+    return _ok(_lib.moe_permute_fwd(ctypes.byref(p), E_tot, _ptr(x), _ptr(topk_idx), _ptr(sorted_token_ids),
+                                    _ptr(num_tokens_post_pad), _ptr(rows), _ptr(pair_row), _ptr(status),
+                                    _stream(stream)), "moe_permute_fwd")
+
+
+def moe_permute_bwd(p: mr_rows_params, grad_rows, pair_row, grad_x, status=None, stream=None) -> int:
+    return _ok(_lib.moe_permute_bwd(ctypes.byref(p), _ptr(grad_rows), _ptr(pair_row), _ptr(grad_x), _ptr(status),
+                                    _stream(stream)), "moe_permute_bwd")
+
+
+def moe_combine_fwd(p: mr_rows_params, rows, pair_row, topk_w, residual, drop_p, rng, out, status=None,
+                    stream=None) -> int:
+    return _ok(_lib.moe_combine_fwd(ctypes.byref(p), _ptr(rows), _ptr(pair_row), _ptr(topk_w), _ptr(residual), drop_p,
+                                    _ptr(rng), _ptr(out), _ptr(status), _stream(stream)), "moe_combine_fwd")
+
+
+def moe_combine_bwd(p: mr_rows_params, grad_out, rows, pair_row, topk_w, sorted_token_ids, num_tokens_post_pad, drop_p,
+                    rng, grad_rows, grad_w, status=None, stream=None) -> int:
+    return _ok(_lib.moe_combine_bwd(ctypes.byref(p), _ptr(grad_out), _ptr(rows), _ptr(pair_row), _ptr(topk_w),
+                                    _ptr(sorted_token_ids), _ptr(num_tokens_post_pad), drop_p, _ptr(rng),
+                                    _ptr(grad_rows), _ptr(grad_w), _ptr(status), _stream(stream)), "moe_combine_bwd")
+
+
+def moe_expert_act_fwd(p: mr_act_params, gu, num_rows, drop_p, rng, h, stream=None) -> int:
+    return _ok(_lib.moe_expert_act_fwd(ctypes.byref(p), _ptr(gu), _ptr(num_rows), drop_p, _ptr(rng), _ptr(h),
+                                       _stream(stream)), "moe_expert_act_fwd")
+
+
+def moe_expert_act_bwd(p: mr_act_params, grad_h, gu, num_rows, drop_p, rng, grad_gu, h=None, stream=None) -> int:
+    return _ok(_lib.moe_expert_act_bwd(ctypes.byref(p), _ptr(grad_h), _ptr(gu), _ptr(num_rows), drop_p, _ptr(rng),
+                                       _ptr(grad_gu), _ptr(h), _stream(stream)), "moe_expert_act_bwd")
+
+
+def moe_dropout_fwd(T, H, dtype, x, residual, drop_p, rng, y, stream=None) -> int:
+    return _ok(_lib.moe_dropout_fwd(T, H, dtype, _ptr(x), _ptr(residual), drop_p, _ptr(rng), _ptr(y), _stream(stream)),
+               "moe_dropout_fwd")
+
+
+def moe_dropout_bwd(T, H, dtype, grad_y, drop_p, rng, grad_x, stream=None) -> int:
+    return _ok(_lib.moe_dropout_bwd(T, H, dtype, _ptr(grad_y), drop_p, _ptr(rng), _ptr(grad_x), _stream(stream)),
+               "moe_dropout_bwd")
 
 
 # ------------------------------------------------------------------- allocating helpers
@@ -718,3 +782,236 @@ def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = N
         _ok(_lib.moe_adapter_proj_fwd(p, x.data_ptr(), w.data_ptr(), pa, pb, pi, ps, out.data_ptr(),
                                       ws.data_ptr() if nb else None, nb, st, raw), "moe_adapter_proj_fwd")
     return out
+
+
+# ------------------------------------------------------------------- rows by expert and back
+# Each step and its gradient are calls of their own, as route() and route_bwd() are: inputs that ask autograd for a
+# gradient are refused instead of giving results that are cut off from them. Buffers may be passed in (a training loop
+# keeps its own); rows behind num_tokens_post_pad are left as they are in those, and undefined in fresh ones.
+
+
+def _explicit_grad(bwd: str, *tensors) -> None:
+    if not torch.is_grad_enabled():
+        return
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise ValueError(f"gradients are computed by {bwd}(): call this under torch.no_grad(), or detach its inputs")
+
+
+_ROW_DTYPES = {torch.float32: MR_F32, torch.bfloat16: MR_BF16}
+
+
+def _row_dtype(what: str, t: torch.Tensor) -> int:
+    code = _ROW_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _check_rng(p: float, rng: Optional[torch.Tensor], device) -> Optional[int]:
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be in [0, 1], got {p}")
+    if rng is None:
+        if p > 0.0:
+            raise ValueError("dropout needs rng, an int64 tensor {seed, offset}")
+        return None
+    _check("rng", rng, (2,), torch.int64, device)
+    return rng.data_ptr()
+
+
+def _check_buffer(what: str, t: Optional[torch.Tensor], shape, dtype, device) -> None:
+    if t is not None:
+        _check(what, t, shape, dtype, device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _rows_plan(T, H, topk, n_rows, dtype):
+    return ctypes.byref(mr_rows_params(T, H, topk, n_rows, dtype))
+
+
+@functools.lru_cache(maxsize=1024)
+def _act_plan(n_rows, I, act, dtype):
+    return ctypes.byref(mr_act_params(n_rows, I, act, dtype))
+
+
+def _check_pairs(name: str, t: torch.Tensor, device):
+    if t.dim() != 2:
+        raise ValueError(f"{name} is [T, topk]")
+    _check(name, t, t.shape, torch.int32, device)
+    return t.shape
+
+
+def permute(x: torch.Tensor, topk_idx: torch.Tensor, E_tot: int, sorted_token_ids: torch.Tensor,
+            num_tokens_post_pad: torch.Tensor, rows: Optional[torch.Tensor] = None,
+            status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """moe_permute_fwd: the tokens' rows in the order of sort() (sorted_token_ids, num_tokens_post_pad) from x [T, H]
+    (fp32 or bf16), zeros at its padding. Gives rows [n_rows, H], n_rows = len(sorted_token_ids), and pair_row [T, topk]
+    (int32), each pair's row or -1."""
+    _explicit_grad("permute_bwd", x, rows)
+    if x.dim() != 2 or sorted_token_ids.dim() != 1:
+        raise ValueError("x is [T, H], sorted_token_ids [n_rows]")
+    (T, H), n, dev = x.shape, sorted_token_ids.shape[0], x.device
+    code = _row_dtype("x", x)
+    _check("x", x, (T, H), x.dtype, dev)
+    k = _check_pairs("topk_idx", topk_idx, dev)[1]
+    _check("topk_idx", topk_idx, (T, k), torch.int32, dev)
+    _check("sorted_token_ids", sorted_token_ids, (n,), torch.int32, dev)
+    _check("num_tokens_post_pad", num_tokens_post_pad, (1,), torch.int32, dev)
+    _check_buffer("rows", rows, (n, H), x.dtype, dev)
+    st = _check_status(status, dev)
+    with _launch(dev, stream) as raw:
+        if rows is None:
+            rows = torch.empty(n, H, dtype=x.dtype, device=dev)
+        pair_row = torch.empty(T, k, dtype=torch.int32, device=dev)
+        _ok(_lib.moe_permute_fwd(_rows_plan(T, H, k, n, code), E_tot, x.data_ptr(), topk_idx.data_ptr(),
+                                 sorted_token_ids.data_ptr(), num_tokens_post_pad.data_ptr(), rows.data_ptr(),
+                                 pair_row.data_ptr(), st, raw), "moe_permute_fwd")
+    return dict(rows=rows, pair_row=pair_row)
+
+
+def _rows_and_pairs(what: str, rows: torch.Tensor, pair_row: torch.Tensor):
+    if rows.dim() != 2:
+        raise ValueError(f"{what} is [n_rows, H]")
+    dev, code = rows.device, _row_dtype(what, rows)
+    _check(what, rows, rows.shape, rows.dtype, dev)
+    T, k = _check_pairs("pair_row", pair_row, dev)
+    return T, k, rows.shape[0], rows.shape[1], dev, code
+
+
+def permute_bwd(grad_rows: torch.Tensor, pair_row: torch.Tensor, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """moe_permute_bwd: grad_x [T, H] from grad_rows [n_rows, H] and permute()'s pair_row."""
+    _explicit_grad("permute", grad_rows)
+    T, k, n, H, dev, code = _rows_and_pairs("grad_rows", grad_rows, pair_row)
+    st = _check_status(status, dev)
+    with _launch(dev, stream) as raw:
+        gx = torch.empty(T, H, dtype=grad_rows.dtype, device=dev)
+        _ok(_lib.moe_permute_bwd(_rows_plan(T, H, k, n, code), grad_rows.data_ptr(), pair_row.data_ptr(),
+                                 gx.data_ptr(), st, raw), "moe_permute_bwd")
+    return gx
+
+
+def combine(rows: torch.Tensor, pair_row: torch.Tensor, topk_w: torch.Tensor, residual: Optional[torch.Tensor] = None,
+            p: float = 0.0, rng: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+            stream=None) -> torch.Tensor:
+    """moe_combine_fwd: out [T, H] = residual + dropout(the sum of each token's rows by topk_w [T, topk], fp32). rng
+    (int64 {seed, offset} on the device) says which elements dropout with probability p takes."""
+    _explicit_grad("combine_bwd", rows, topk_w, residual)
+    T, k, n, H, dev, code = _rows_and_pairs("rows", rows, pair_row)
+    _check("topk_w", topk_w, (T, k), torch.float32, dev)
+    if residual is not None:
+        _check("residual", residual, (T, H), rows.dtype, dev)
+    r, st = _check_rng(p, rng, dev), _check_status(status, dev)
+    with _launch(dev, stream) as raw:
+        out = torch.empty(T, H, dtype=rows.dtype, device=dev)
+        _ok(_lib.moe_combine_fwd(_rows_plan(T, H, k, n, code), rows.data_ptr(), pair_row.data_ptr(), topk_w.data_ptr(),
+                                 None if residual is None else residual.data_ptr(), p, r, out.data_ptr(), st, raw),
+            "moe_combine_fwd")
+    return out
+
+
+def combine_bwd(grad_out: torch.Tensor, rows: torch.Tensor, pair_row: torch.Tensor, topk_w: torch.Tensor,
+                sorted_token_ids: torch.Tensor, num_tokens_post_pad: torch.Tensor, p: float = 0.0,
+                rng: Optional[torch.Tensor] = None, grad_rows: Optional[torch.Tensor] = None,
+                status: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """moe_combine_bwd: grad_rows [n_rows, H] (zeros at padding) and grad_w [T, topk] (fp32) of combine() with the same
+    rows, weights, p and rng. The residual's gradient is grad_out."""
+    _explicit_grad("combine", grad_out, rows, topk_w, grad_rows)
+    T, k, n, H, dev, code = _rows_and_pairs("rows", rows, pair_row)
+    _check("grad_out", grad_out, (T, H), rows.dtype, dev)
+    _check("topk_w", topk_w, (T, k), torch.float32, dev)
+    _check("sorted_token_ids", sorted_token_ids, (n,), torch.int32, dev)
+    _check("num_tokens_post_pad", num_tokens_post_pad, (1,), torch.int32, dev)
+    _check_buffer("grad_rows", grad_rows, (n, H), rows.dtype, dev)
+    r, st = _check_rng(p, rng, dev), _check_status(status, dev)
+    with _launch(dev, stream) as raw:
+        if grad_rows is None:
+            grad_rows = torch.empty_like(rows)
+        grad_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        _ok(_lib.moe_combine_bwd(_rows_plan(T, H, k, n, code), grad_out.data_ptr(), rows.data_ptr(),
+                                 pair_row.data_ptr(), topk_w.data_ptr(), sorted_token_ids.data_ptr(),
+                                 num_tokens_post_pad.data_ptr(), p, r, grad_rows.data_ptr(), grad_w.data_ptr(), st,
+                                 raw), "moe_combine_bwd")
+    return dict(grad_rows=grad_rows, grad_w=grad_w)
+
+
+def _check_gated(gu: torch.Tensor, num_rows):
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError("gu is [n_rows, 2 * I]")
+    dev, code = gu.device, _row_dtype("gu", gu)
+    _check("gu", gu, gu.shape, gu.dtype, dev)
+    if num_rows is not None:
+        _check("num_rows", num_rows, (1,), torch.int32, dev)
+    return gu.shape[0], gu.shape[1] // 2, dev, code, None if num_rows is None else num_rows.data_ptr()
+
+
+def expert_act(gu: torch.Tensor, num_rows: Optional[torch.Tensor] = None, act: int = MR_SILU, p: float = 0.0,
+               rng: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_expert_act_fwd: h [n_rows, I] = dropout(act(gate) * up) of gu [n_rows, 2*I] (a row's gate values, then its up
+    values), for the first num_rows rows (int32 on the device, sort()'s num_tokens_post_pad; None: all)."""
+    _explicit_grad("expert_act_bwd", gu, h)
+    n, I, dev, code, used = _check_gated(gu, num_rows)
+    _check_buffer("h", h, (n, I), gu.dtype, dev)
+    r = _check_rng(p, rng, dev)
+    with _launch(dev, stream) as raw:
+        if h is None:
+            h = torch.empty(n, I, dtype=gu.dtype, device=dev)
+        _ok(_lib.moe_expert_act_fwd(_act_plan(n, I, act, code), gu.data_ptr(), used, p, r, h.data_ptr(), raw),
+            "moe_expert_act_fwd")
+    return h
+
+
+def expert_act_bwd(grad_h: torch.Tensor, gu: torch.Tensor, num_rows: Optional[torch.Tensor] = None,
+                   act: int = MR_SILU, p: float = 0.0, rng: Optional[torch.Tensor] = None,
+                   grad_gu: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None, need_h: bool = True,
+                   stream=None) -> dict:
+    """moe_expert_act_bwd: grad_gu [n_rows, 2*I] of expert_act() with the same gu, p and rng, and (unless need_h is
+    False) its h, computed again for the gradient of the weights behind it."""
+    _explicit_grad("expert_act", grad_h, gu, grad_gu, h)
+    n, I, dev, code, used = _check_gated(gu, num_rows)
+    _check("grad_h", grad_h, (n, I), gu.dtype, dev)
+    _check_buffer("grad_gu", grad_gu, gu.shape, gu.dtype, dev)
+    _check_buffer("h", h, (n, I), gu.dtype, dev)
+    r = _check_rng(p, rng, dev)
+    with _launch(dev, stream) as raw:
+        out = dict(grad_gu=torch.empty_like(gu) if grad_gu is None else grad_gu)
+        if need_h:
+            out["h"] = torch.empty_like(grad_h) if h is None else h
+        _ok(_lib.moe_expert_act_bwd(_act_plan(n, I, act, code), grad_h.data_ptr(), gu.data_ptr(), used, p, r,
+                                    out["grad_gu"].data_ptr(), out["h"].data_ptr() if need_h else None, raw),
+            "moe_expert_act_bwd")
+    return out
+
+
+def _check_hidden(what: str, x: torch.Tensor):
+    if x.dim() != 2:
+        raise ValueError(f"{what} is [T, H]")
+    code = _row_dtype(what, x)
+    _check(what, x, x.shape, x.dtype, x.device)
+    return x.shape[0], x.shape[1], x.device, code
+
+
+def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Optional[torch.Tensor] = None,
+            stream=None) -> torch.Tensor:
+    """moe_dropout_fwd: residual + dropout(x) for x [T, H] (fp32 or bf16). rng as for combine()."""
+    _explicit_grad("dropout_bwd", x, residual)
+    T, H, dev, code = _check_hidden("x", x)
+    if residual is not None:
+        _check("residual", residual, (T, H), x.dtype, dev)
+    r = _check_rng(p, rng, dev)
+    with _launch(dev, stream) as raw:
+        y = torch.empty_like(x)
+        _ok(_lib.moe_dropout_fwd(T, H, code, x.data_ptr(), None if residual is None else residual.data_ptr(), p, r,
+                                 y.data_ptr(), raw), "moe_dropout_fwd")
+    return y
+
+
+def dropout_bwd(grad_y: torch.Tensor, p: float, rng: Optional[torch.Tensor], stream=None) -> torch.Tensor:
+    """moe_dropout_bwd: the gradient of dropout()'s x with the same p and rng. The residual's is grad_y."""
+    _explicit_grad("dropout", grad_y)
+    T, H, dev, code = _check_hidden("grad_y", grad_y)
+    r = _check_rng(p, rng, dev)
+    with _launch(dev, stream) as raw:
+        gx = torch.empty_like(grad_y)
+        _ok(_lib.moe_dropout_bwd(T, H, code, grad_y.data_ptr(), p, r, gx.data_ptr(), raw), "moe_dropout_bwd")
+    return gx

@@ -2,7 +2,7 @@
 
 Translation units compile in parallel (fwd.cu and layer_few.cu once per score
 function x logits dtype, plus sort.cu, bwd.cu, aux_loss.cu, experts.cu, experts_mma.cu,
-adapter_mma.cu, api.cu) and link into one shared library with the
+adapter_mma.cu, rows.cu, act.cu, api.cu) and link into one shared library with the
 static CUDA runtime, so loading it needs no CUDA library path.
 
     python -m top_gating_expert_row_gb300.build [--verbose]
@@ -41,6 +41,8 @@ UNITS = [
     ("experts", "experts.cu", []),
     ("experts_mma", "experts_mma.cu", []),
     ("adapter_mma", "adapter_mma.cu", []),
+    ("rows", "rows.cu", []),
+    ("act", "act.cu", []),
     ("api", "api.cu", []),
 ]
 

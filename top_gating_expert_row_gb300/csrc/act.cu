@@ -1,0 +1,250 @@
+// The gated activation of the experts' rows with expert dropout, and dropout of hidden states, with their gradients:
+// moe_expert_act_fwd / bwd and moe_dropout_fwd / bwd.
+//
+//   h = m * act(g) * u                                    for the rows (g, u) in use; m: dropout's factors (rows.cuh)
+//   d = m * grad_h:  grad_u = d act(g),  grad_g = d u act'(g);  h again where it is asked for
+//   y = residual + m * x;  grad_x = m * grad_y
+//   SiLU: act = g s, act' = s + g s (1 - s), s = 1 / (1 + exp -g);  GELU: act = g Phi(g), act' = Phi(g) + g phi(g)
+// Bound by memory, but for what the generator and erfc cost in bf16.
+#include <climits>
+
+#include "rows.cuh"
+
+namespace mr {
+namespace {
+
+// act(g) and act'(g) in fp32. The sigmoid is a hardware exponential (of the two-part product, exp_value) and
+// reciprocal: 1 to 2 units of the last place. Phi(g) = erfc(-g / sqrt 2) / 2 keeps its bits for g below zero.
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float gate(float g, float& da)
+{
+    if constexpr (ACT == MR_SILU) {
+        const float s = __fdividef(1.0f, 1.0f + exp_value(-g)), a = g * s;
+        if constexpr (GRAD) da = fmaf(a, 1.0f - s, s);
+        return a;
+    } else {
+        const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+        if constexpr (GRAD) da = fmaf(g, 0.39894228040143268f * exp_value(-0.5f * g * g), cdf);
+        return g * cdf;
+    }
+}
+
+struct ActArgs {
+    const void* grad_h;  // backward only
+    const void* gu;
+    const int32_t* used;  // null: all n_rows
+    void* grad_gu;        // backward only
+    void* h;              // backward: nullable
+    DropArgs drop;
+    int n_rows, W, wc;
+};
+
+template <typename T, bool VEC, int ACT, bool DROP, bool BWD>
+__global__ void __launch_bounds__(kRowsThreads) k_act(const __grid_constant__ ActArgs a)
+{
+    pdl_trigger_small();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int across = 1 << a.wc, tall = (kRowsThreads / 32) >> a.wc;
+    const int c0 = (static_cast<int>(blockIdx.y) * across + (warp & (across - 1))) * kSpan;
+    if (c0 >= a.W) return;
+    const int rows = a.used ? min(__ldcg(a.used), a.n_rows) : a.n_rows;
+    DropState ds;
+    if constexpr (DROP) ds = drop_state(a.drop);
+    for (long long r = static_cast<long long>(blockIdx.x) * tall + (warp >> a.wc); r < rows;
+         r += static_cast<long long>(gridDim.x) * tall) {
+        const T* gu = static_cast<const T*>(a.gu) + r * 2 * a.W;
+        Pack<T> pg, pu, pd;
+        load_span<VEC>(gu, c0, a.W, lane, pg);
+        load_span<VEC>(gu + a.W, c0, a.W, lane, pu);
+        if constexpr (BWD) load_span<VEC>(static_cast<const T*>(a.grad_h) + r * a.W, c0, a.W, lane, pd);
+        if constexpr (!BWD) {
+            float v[8], da;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = gate<ACT, false>(pg.get(e), da) * pu.get(e);
+            if constexpr (DROP) drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(r), c0, lane, v);
+            Pack<T> q;
+            q.set(v);
+            store_span<VEC>(static_cast<T*>(a.h) + r * a.W, c0, a.W, lane, q);
+        } else {
+            float m[8], v[8], gg[8], gq[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[e] = 1.0f;
+            if constexpr (DROP) drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(r), c0, lane, m);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float da;
+                const float act = gate<ACT, true>(pg.get(e), da), u = pu.get(e);
+                // a dropped element is 0 whatever it held
+                const float d = !DROP || m[e] != 0.0f ? m[e] * pd.get(e) : 0.0f;
+                v[e] = !DROP || m[e] != 0.0f ? m[e] * act * u : 0.0f;
+                gq[e] = !DROP || m[e] != 0.0f ? d * act : 0.0f;
+                gg[e] = !DROP || m[e] != 0.0f ? d * u * da : 0.0f;
+            }
+            T* grad = static_cast<T*>(a.grad_gu) + r * 2 * a.W;
+            Pack<T> q;
+            q.set(gg);
+            store_span<VEC>(grad, c0, a.W, lane, q);
+            q.set(gq);
+            store_span<VEC>(grad + a.W, c0, a.W, lane, q);
+            if (a.h) {
+                q.set(v);
+                store_span<VEC>(static_cast<T*>(a.h) + r * a.W, c0, a.W, lane, q);
+            }
+        }
+    }
+}
+
+struct DropoutArgs {
+    const void* x;
+    const void* residual;  // nullable
+    void* y;
+    DropArgs drop;
+    int T, W, wc;
+};
+
+template <typename T, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kRowsThreads) k_dropout(const __grid_constant__ DropoutArgs a)
+{
+    pdl_trigger_small();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int across = 1 << a.wc, tall = (kRowsThreads / 32) >> a.wc;
+    const int c0 = (static_cast<int>(blockIdx.y) * across + (warp & (across - 1))) * kSpan;
+    if (c0 >= a.W) return;
+    DropState ds;
+    if constexpr (DROP) ds = drop_state(a.drop);
+    for (long long t = static_cast<long long>(blockIdx.x) * tall + (warp >> a.wc); t < a.T;
+         t += static_cast<long long>(gridDim.x) * tall) {
+        Pack<T> p, q;
+        load_span<VEC>(static_cast<const T*>(a.x) + t * a.W, c0, a.W, lane, p);
+        if (a.residual) load_span<VEC>(static_cast<const T*>(a.residual) + t * a.W, c0, a.W, lane, q);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = p.get(e);
+        if constexpr (DROP) drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(t), c0, lane, v);
+        if (a.residual) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += q.get(e);
+        }
+        q.set(v);
+        store_span<VEC>(static_cast<T*>(a.y) + t * a.W, c0, a.W, lane, q);
+    }
+}
+
+// ---- host --------------------------------------------------------------------
+
+// Launches a kernel whose warps take a row and a span at a time.
+template <typename Args>
+int launch_spans(void (*kernel)(Args), Args a, long long rows, cudaStream_t st)
+{
+    const int spans = spans_of(a.W);
+    a.wc = warps_across(spans);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(kernel), rows, spans, a.wc);
+    if (grid.x < 1) return MR_ECUDA;
+    return launch_kernel(kernel, grid, dim3(kRowsThreads), 0, st, 0, a) == cudaSuccess ? MR_OK : MR_ECUDA;
+}
+
+template <typename T, int ACT, bool BWD>
+int act_of(const ActArgs& a, cudaStream_t st)
+{
+    const size_t n = kVecBytes<T>;
+    const bool vec = a.W % 8 == 0 && at_multiple(a.gu, n) && at_multiple(a.h, n) && at_multiple(a.grad_h, n) &&
+                     at_multiple(a.grad_gu, n);
+    if (a.drop.cut)
+        return vec ? launch_spans(k_act<T, true, ACT, true, BWD>, a, a.n_rows, st)
+                   : launch_spans(k_act<T, false, ACT, true, BWD>, a, a.n_rows, st);
+    return vec ? launch_spans(k_act<T, true, ACT, false, BWD>, a, a.n_rows, st)
+               : launch_spans(k_act<T, false, ACT, false, BWD>, a, a.n_rows, st);
+}
+
+template <bool BWD>
+int act_call(const ActArgs& a, int act, int dtype, cudaStream_t st)
+{
+    using B = __nv_bfloat16;
+    if (act == MR_SILU) return dtype == MR_F32 ? act_of<float, MR_SILU, BWD>(a, st) : act_of<B, MR_SILU, BWD>(a, st);
+    return dtype == MR_F32 ? act_of<float, MR_GELU, BWD>(a, st) : act_of<B, MR_GELU, BWD>(a, st);
+}
+
+template <typename T>
+int dropout_of(const DropoutArgs& a, cudaStream_t st)
+{
+    const size_t n = kVecBytes<T>;
+    const bool vec = a.W % 8 == 0 && at_multiple(a.x, n) && at_multiple(a.residual, n) && at_multiple(a.y, n);
+    if (a.drop.cut)
+        return vec ? launch_spans(k_dropout<T, true, true>, a, a.T, st) : launch_spans(k_dropout<T, false, true>, a, a.T, st);
+    return vec ? launch_spans(k_dropout<T, true, false>, a, a.T, st) : launch_spans(k_dropout<T, false, false>, a, a.T, st);
+}
+
+int check_act(const mr_act_params* p)
+{
+    if (!p || p->n_rows < 0 || p->I < 1) return MR_EINVAL;
+    if (p->act != MR_SILU && p->act != MR_GELU) return MR_EINVAL;
+    if (p->dtype != MR_F32 && p->dtype != MR_BF16) return MR_EINVAL;
+    return p->I > MR_MAX_WIDTH ? MR_EUNSUPPORTED : MR_OK;
+}
+
+int dropout_call(int T, int H, int dtype, const void* x, const void* residual, float drop_p, const void* rng, void* y,
+                 cudaStream_t st)
+{
+    if (T < 0 || H < 1 || (dtype != MR_F32 && dtype != MR_BF16)) return MR_EINVAL;
+    if (H > MR_MAX_WIDTH) return MR_EUNSUPPORTED;
+    DropArgs drop;
+    if (!drop_args(drop_p, rng, drop)) return MR_EINVAL;
+    if (T == 0) return MR_OK;
+    const size_t size = element(dtype);
+    if (!x || !y || !at_multiple(x, size) || !at_multiple(y, size) || !at_multiple(residual, size)) return MR_EINVAL;
+    const DropoutArgs a = {x, residual, y, drop, T, H, 0};
+    return dtype == MR_F32 ? dropout_of<float>(a, st) : dropout_of<__nv_bfloat16>(a, st);
+}
+
+}  // namespace
+}  // namespace mr
+
+using namespace mr;
+
+extern "C" {
+
+int moe_expert_act_fwd(const mr_act_params* p, const void* gu, const int32_t* num_rows, float drop_p, const void* rng,
+                       void* h, mr_stream_t stream)
+{
+    const int rc = check_act(p);
+    if (rc != MR_OK) return rc;
+    DropArgs drop;
+    if (!drop_args(drop_p, rng, drop)) return MR_EINVAL;
+    if (p->n_rows == 0) return MR_OK;
+    const size_t size = element(p->dtype);
+    if (!gu || !h || !at_multiple(gu, size) || !at_multiple(h, size) || !at_multiple(num_rows, 4)) return MR_EINVAL;
+    const ActArgs a = {nullptr, gu, num_rows, nullptr, h, drop, p->n_rows, p->I, 0};
+    return act_call<false>(a, p->act, p->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_expert_act_bwd(const mr_act_params* p, const void* grad_h, const void* gu, const int32_t* num_rows, float drop_p,
+                       const void* rng, void* grad_gu, void* h, mr_stream_t stream)
+{
+    const int rc = check_act(p);
+    if (rc != MR_OK) return rc;
+    DropArgs drop;
+    if (!drop_args(drop_p, rng, drop)) return MR_EINVAL;
+    if (p->n_rows == 0) return MR_OK;
+    const size_t size = element(p->dtype);
+    if (!grad_h || !gu || !grad_gu || !at_multiple(grad_h, size) || !at_multiple(gu, size) || !at_multiple(grad_gu, size) ||
+        !at_multiple(h, size) || !at_multiple(num_rows, 4))
+        return MR_EINVAL;
+    const ActArgs a = {grad_h, gu, num_rows, grad_gu, h, drop, p->n_rows, p->I, 0};
+    return act_call<true>(a, p->act, p->dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_dropout_fwd(int T, int H, int dtype, const void* x, const void* residual, float drop_p, const void* rng, void* y,
+                    mr_stream_t stream)
+{
+    return dropout_call(T, H, dtype, x, residual, drop_p, rng, y, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_dropout_bwd(int T, int H, int dtype, const void* grad_y, float drop_p, const void* rng, void* grad_x,
+                    mr_stream_t stream)
+{
+    return dropout_call(T, H, dtype, grad_y, nullptr, drop_p, rng, grad_x, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,390 @@
+// Tokens to rows sorted by expert and back, with their gradients: moe_permute_fwd / bwd and moe_combine_fwd / bwd.
+//
+//   rows[r(t,j)] = x[t], 0 at the sort's padding                 (permute; its gradient sums a token's rows)
+//   out[t] = residual[t] + m[t] * sum_j w[t,j] rows[r(t,j)]      (combine; m: dropout's factors, see rows.cuh)
+//   g = m[t] grad_out[t]:  grad_rows[r(t,j)] = w[t,j] g,  grad_w[t,j] = <g, rows[r(t,j)]>
+// All are bound by memory. A token's slots are summed in slot order in fp32 and rounded once: no atomics, the same
+// bits each time.
+#include <climits>
+
+#include "rows.cuh"
+
+namespace mr {
+namespace {
+
+// ---- permute ---------------------------------------------------------------
+
+struct PermuteArgs {
+    const void* x;
+    const int32_t* topk_idx;
+    const int32_t* ids;
+    const int32_t* npp;
+    void* rows;
+    int32_t* pair_row;
+    int32_t* status;
+    int P, topk, n_rows, E_tot;
+    int words;  // of a row
+    int wc;
+};
+
+// A warp copies 32 * N words of a row, all of its loads in flight before the first store.
+template <typename Word, int N>
+__global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant__ PermuteArgs a)
+{
+    pdl_trigger_small();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int across = 1 << a.wc, tall = (kRowsThreads / 32) >> a.wc;
+    const int first = (static_cast<int>(blockIdx.y) * across + (warp & (across - 1))) * 32 * N;
+    if (blockIdx.y == 0) {
+        for (long long i = static_cast<long long>(blockIdx.x) * kRowsThreads + threadIdx.x; i < a.P;
+             i += static_cast<long long>(gridDim.x) * kRowsThreads) {
+            const int e = __ldcg(a.topk_idx + i);
+            if (e < 0 || e >= a.E_tot) a.pair_row[i] = -1;
+        }
+    }
+    int rows = __ldcg(a.npp);
+    if (rows > a.n_rows) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_status(a.status, kStatusRange);
+        rows = a.n_rows;
+    }
+    if (first >= a.words) return;
+    for (long long r = static_cast<long long>(blockIdx.x) * tall + (warp >> a.wc); r < rows;
+         r += static_cast<long long>(gridDim.x) * tall) {
+        const int id = __ldcg(a.ids + r);
+        const bool real = id >= 0 && id < a.P;
+        Word v[N];
+        const Word* src = static_cast<const Word*>(a.x) + static_cast<long long>(real ? id / a.topk : 0) * a.words;
+        Word* dst = static_cast<Word*>(a.rows) + r * a.words;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = first + 32 * i + lane;
+            v[i] = Word{};
+            if (real && c < a.words) v[i] = src[c];
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = first + 32 * i + lane;
+            if (c < a.words) dst[c] = v[i];
+        }
+        if (first == 0 && lane == 0) {
+            if (real) a.pair_row[id] = static_cast<int32_t>(r);
+            else if (id != a.P) report_status(a.status, kStatusRange);
+        }
+    }
+}
+
+// ---- a token's rows, summed ------------------------------------------------
+
+struct CombineArgs {
+    const void* rows;
+    const int32_t* pair_row;
+    const float* w;         // null: ones
+    const void* residual;   // null: none
+    void* out;
+    int32_t* status;
+    DropArgs drop;
+    int T, topk, n_rows, W, wc;
+};
+
+// A warp sums a span of a token: the rows' numbers and weights a lane each, then the rows eight at a time.
+template <typename T, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kRowsThreads) k_combine(const __grid_constant__ CombineArgs a)
+{
+    constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
+    pdl_trigger_small();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int across = 1 << a.wc, tall = (kRowsThreads / 32) >> a.wc;
+    const int c0 = (static_cast<int>(blockIdx.y) * across + (warp & (across - 1))) * kSpan;
+    if (c0 >= a.W) return;
+    const T* rows = static_cast<const T*>(a.rows);
+    DropState ds;
+    if constexpr (DROP) ds = drop_state(a.drop);
+    for (long long t = static_cast<long long>(blockIdx.x) * tall + (warp >> a.wc); t < a.T;
+         t += static_cast<long long>(gridDim.x) * tall) {
+        Pack<T> q;
+        float v[8] = {};
+        for (int j0 = 0; j0 < a.topk; j0 += 32) {
+            int r = -1;
+            float w = 1.0f;
+            if (j0 + lane < a.topk) {
+                r = __ldcg(a.pair_row + t * a.topk + j0 + lane);
+                if (a.w) w = __ldcg(a.w + t * a.topk + j0 + lane);
+                if (r < -1 || r >= a.n_rows) {
+                    report_status(a.status, kStatusRange);
+                    r = -1;
+                }
+            }
+            const int n = min(32, a.topk - j0);
+            for (int j = 0; j < n; j += kBatch) {
+                Pack<T> p[kBatch];
+                int rj[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    rj[i] = __shfl_sync(kFull, r, (j + i) & 31);
+                    if (j + i >= n) rj[i] = -1;
+                    if (rj[i] >= 0) load_span<VEC>(rows + static_cast<long long>(rj[i]) * a.W, c0, a.W, lane, p[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float wj = __shfl_sync(kFull, w, (j + i) & 31);
+                    if (rj[i] < 0) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = fmaf(wj, p[i].get(e), v[e]);
+                }
+            }
+        }
+        if constexpr (DROP) drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(t), c0, lane, v);
+        if (a.residual) {
+            Pack<T> p;
+            load_span<VEC>(static_cast<const T*>(a.residual) + t * a.W, c0, a.W, lane, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += p.get(e);
+        }
+        q.set(v);
+        store_span<VEC>(static_cast<T*>(a.out) + t * a.W, c0, a.W, lane, q);
+    }
+}
+
+// ---- the weighted sum's gradient ---------------------------------------------
+
+struct CombineBwdArgs {
+    const void* grad_out;
+    const void* rows;
+    const int32_t* pair_row;
+    const float* w;
+    const int32_t* ids;
+    const int32_t* npp;
+    void* grad_rows;
+    float* grad_w;
+    int32_t* status;
+    DropArgs drop;
+    int T, topk, n_rows, W;
+};
+
+// A warp per pair, a token's pairs side by side so that its gradient comes from L2 or L1 after the first; behind the
+// pairs a warp per 32 sorted positions, which zeroes the padding rows among them.
+template <typename T, bool VEC, bool DROP>
+__global__ void __launch_bounds__(kRowsThreads) k_combine_bwd(const __grid_constant__ CombineBwdArgs a)
+{
+    constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
+    pdl_trigger_small();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long P = static_cast<long long>(a.T) * a.topk, warps = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
+    const long long units = P + (a.n_rows + 31) / 32;
+    DropState ds;
+    if constexpr (DROP) ds = drop_state(a.drop);
+    for (long long u = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+        if (u >= P) {
+            const long long pos = (u - P) * 32 + lane;
+            const int rows = min(__ldcg(a.npp), a.n_rows);
+            bool pad = false;
+            if (pos < rows) {
+                const int id = __ldcg(a.ids + pos);
+                pad = id < 0 || id >= P;
+            }
+            for (unsigned m = __ballot_sync(kFull, pad); m; m &= m - 1) {
+                T* row = static_cast<T*>(a.grad_rows) + (pos - lane + __ffs(m) - 1) * a.W;
+                const Pack<T> zero = {};
+                for (int c0 = 0; c0 < a.W; c0 += kSpan) store_span<VEC>(row, c0, a.W, lane, zero);
+            }
+            continue;
+        }
+        int r = __ldcg(a.pair_row + u);
+        const float w = __ldcg(a.w + u);
+        if (r < -1 || r >= a.n_rows) {
+            if (lane == 0) report_status(a.status, kStatusRange);
+            r = -1;
+        }
+        float dot = 0.0f;
+        if (r >= 0) {
+            const uint32_t t = static_cast<uint32_t>(u / a.topk);
+            const T* g = static_cast<const T*>(a.grad_out) + static_cast<long long>(t) * a.W;
+            const T* row = static_cast<const T*>(a.rows) + static_cast<long long>(r) * a.W;
+            T* grad = static_cast<T*>(a.grad_rows) + static_cast<long long>(r) * a.W;
+            for (int c = 0; c < a.W; c += kBatch * kSpan) {
+                Pack<T> pg[kBatch], pr[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    load_span<VEC>(row, c + i * kSpan, a.W, lane, pr[i]);
+                    load_span<VEC>(g, c + i * kSpan, a.W, lane, pg[i], false);
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int c0 = c + i * kSpan;
+                    if (c0 >= a.W) break;
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = pg[i].get(e);
+                    if constexpr (DROP) drop_span<VEC>(a.drop, ds, t, c0, lane, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dot = fmaf(v[e], pr[i].get(e), dot);
+                        v[e] *= w;
+                    }
+                    Pack<T> q;
+                    q.set(v);
+                    store_span<VEC>(grad, c0, a.W, lane, q);
+                }
+            }
+        }
+        dot = warp_sum(dot);
+        if (lane == 0) a.grad_w[u] = dot;
+    }
+}
+
+// ---- host --------------------------------------------------------------------
+
+int check_rows(const mr_rows_params* p)
+{
+    if (!p) return MR_EINVAL;
+    if (p->T < 0 || p->H < 1 || p->topk < 1 || p->n_rows < 0) return MR_EINVAL;
+    if (p->dtype != MR_F32 && p->dtype != MR_BF16) return MR_EINVAL;
+    if (static_cast<long long>(p->T) * p->topk >= INT_MAX) return MR_EINVAL;
+    return p->H > MR_MAX_WIDTH ? MR_EUNSUPPORTED : MR_OK;
+}
+
+template <typename Word, int N>
+int permute(PermuteArgs a, size_t row_bytes, cudaStream_t st)
+{
+    a.words = static_cast<int>(row_bytes / sizeof(Word));
+    const int spans = (a.words + 32 * N - 1) / (32 * N);
+    a.wc = warps_across(spans);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_permute<Word, N>), a.n_rows, spans, a.wc);
+    if (grid.x < 1) return MR_ECUDA;
+    const int e = launch_kernel(k_permute<Word, N>, grid, dim3(kRowsThreads), 0, st, 0, a);
+    return e == cudaSuccess ? MR_OK : MR_ECUDA;
+}
+
+template <typename T, bool VEC, bool DROP>
+int combine(CombineArgs a, cudaStream_t st)
+{
+    const int spans = spans_of(a.W);
+    a.wc = warps_across(spans);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_combine<T, VEC, DROP>), a.T, spans, a.wc);
+    if (grid.x < 1) return MR_ECUDA;
+    const int e = launch_kernel(k_combine<T, VEC, DROP>, grid, dim3(kRowsThreads), 0, st, 0, a);
+    return e == cudaSuccess ? MR_OK : MR_ECUDA;
+}
+
+template <typename T>
+int combine_of(const CombineArgs& a, cudaStream_t st)
+{
+    const size_t n = kVecBytes<T>;
+    const bool vec = a.W % 8 == 0 && at_multiple(a.rows, n) && at_multiple(a.out, n) && at_multiple(a.residual, n);
+    if (a.drop.cut) return vec ? combine<T, true, true>(a, st) : combine<T, false, true>(a, st);
+    return vec ? combine<T, true, false>(a, st) : combine<T, false, false>(a, st);
+}
+
+template <typename T, bool VEC, bool DROP>
+int combine_bwd(const CombineBwdArgs& a, cudaStream_t st)
+{
+    const long long warps = static_cast<long long>(a.T) * a.topk + (a.n_rows + 31) / 32;
+    const int g = persistent_grid(reinterpret_cast<const void*>(k_combine_bwd<T, VEC, DROP>), kRowsThreads, 0,
+                                  (warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32), true);
+    if (g < 1) return MR_ECUDA;
+    const int e = launch_kernel(k_combine_bwd<T, VEC, DROP>, dim3(g), dim3(kRowsThreads), 0, st, 0, a);
+    return e == cudaSuccess ? MR_OK : MR_ECUDA;
+}
+
+template <typename T>
+int combine_bwd_of(const CombineBwdArgs& a, cudaStream_t st)
+{
+    const size_t n = kVecBytes<T>;
+    const bool vec = a.W % 8 == 0 && at_multiple(a.rows, n) && at_multiple(a.grad_out, n) && at_multiple(a.grad_rows, n);
+    if (a.drop.cut) return vec ? combine_bwd<T, true, true>(a, st) : combine_bwd<T, false, true>(a, st);
+    return vec ? combine_bwd<T, true, false>(a, st) : combine_bwd<T, false, false>(a, st);
+}
+
+int combine_call(const mr_rows_params& p, const void* rows, const int32_t* pair_row, const float* w, const void* residual,
+                 const DropArgs& drop, void* out, int32_t* status, cudaStream_t st)
+{
+    const CombineArgs a = {rows, pair_row, w, residual, out, status, drop, p.T, p.topk, p.n_rows, p.H, 0};
+    return p.dtype == MR_F32 ? combine_of<float>(a, st) : combine_of<__nv_bfloat16>(a, st);
+}
+
+}  // namespace
+}  // namespace mr
+
+using namespace mr;
+
+extern "C" {
+
+int moe_permute_fwd(const mr_rows_params* p, int E_tot, const void* x, const int32_t* topk_idx,
+                    const int32_t* sorted_token_ids, const int32_t* num_tokens_post_pad, void* rows, int32_t* pair_row,
+                    int32_t* status, mr_stream_t stream)
+{
+    const int rc = check_rows(p);
+    if (rc != MR_OK) return rc;
+    if (E_tot < 1) return MR_EINVAL;
+    if (p->T == 0) return MR_OK;
+    const size_t size = element(p->dtype);
+    if (!x || !topk_idx || !num_tokens_post_pad || !pair_row || (p->n_rows > 0 && (!sorted_token_ids || !rows))) return MR_EINVAL;
+    if (!at_multiple(x, size) || !at_multiple(rows, size) || !at_multiple(topk_idx, 4) || !at_multiple(sorted_token_ids, 4) ||
+        !at_multiple(num_tokens_post_pad, 4) || !at_multiple(pair_row, 4) || !at_multiple(status, 4))
+        return MR_EINVAL;
+    const PermuteArgs a = {x, topk_idx, sorted_token_ids, num_tokens_post_pad, rows, pair_row, status,
+                           p->T * p->topk, p->topk, p->n_rows, E_tot, 0, 0};
+    const size_t bytes = size * p->H;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    auto fits = [&](size_t n) { return bytes % n == 0 && at_multiple(x, n) && at_multiple(rows, n); };
+    if (fits(16)) return permute<uint4, 4>(a, bytes, st);
+    return fits(4) ? permute<uint32_t, 8>(a, bytes, st) : permute<uint16_t, 8>(a, bytes, st);
+}
+
+int moe_permute_bwd(const mr_rows_params* p, const void* grad_rows, const int32_t* pair_row, void* grad_x,
+                    int32_t* status, mr_stream_t stream)
+{
+    const int rc = check_rows(p);
+    if (rc != MR_OK) return rc;
+    if (p->T == 0) return MR_OK;
+    const size_t size = element(p->dtype);
+    if ((p->n_rows > 0 && !grad_rows) || !pair_row || !grad_x) return MR_EINVAL;
+    if (!at_multiple(grad_rows, size) || !at_multiple(grad_x, size) || !at_multiple(pair_row, 4) || !at_multiple(status, 4))
+        return MR_EINVAL;
+    return combine_call(*p, grad_rows, pair_row, nullptr, nullptr, DropArgs{nullptr, 0, 1.0f}, grad_x, status,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_combine_fwd(const mr_rows_params* p, const void* rows, const int32_t* pair_row, const float* topk_w,
+                    const void* residual, float drop_p, const void* rng, void* out, int32_t* status, mr_stream_t stream)
+{
+    const int rc = check_rows(p);
+    if (rc != MR_OK) return rc;
+    DropArgs drop;
+    if (!drop_args(drop_p, rng, drop)) return MR_EINVAL;
+    if (p->T == 0) return MR_OK;
+    const size_t size = element(p->dtype);
+    if ((p->n_rows > 0 && !rows) || !pair_row || !topk_w || !out) return MR_EINVAL;
+    if (!at_multiple(rows, size) || !at_multiple(out, size) || !at_multiple(residual, size) || !at_multiple(pair_row, 4) ||
+        !at_multiple(topk_w, 4) || !at_multiple(status, 4))
+        return MR_EINVAL;
+    return combine_call(*p, rows, pair_row, topk_w, residual, drop, out, status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_combine_bwd(const mr_rows_params* p, const void* grad_out, const void* rows, const int32_t* pair_row,
+                    const float* topk_w, const int32_t* sorted_token_ids, const int32_t* num_tokens_post_pad,
+                    float drop_p, const void* rng, void* grad_rows, float* grad_w, int32_t* status, mr_stream_t stream)
+{
+    const int rc = check_rows(p);
+    if (rc != MR_OK) return rc;
+    DropArgs drop;
+    if (!drop_args(drop_p, rng, drop)) return MR_EINVAL;
+    if (p->T == 0) return MR_OK;
+    const size_t size = element(p->dtype);
+    if (!grad_out || !pair_row || !topk_w || !num_tokens_post_pad || !grad_w ||
+        (p->n_rows > 0 && (!rows || !grad_rows || !sorted_token_ids)))
+        return MR_EINVAL;
+    if (!at_multiple(grad_out, size) || !at_multiple(rows, size) || !at_multiple(grad_rows, size) || !at_multiple(pair_row, 4) ||
+        !at_multiple(topk_w, 4) || !at_multiple(sorted_token_ids, 4) || !at_multiple(num_tokens_post_pad, 4) ||
+        !at_multiple(grad_w, 4) || !at_multiple(status, 4))
+        return MR_EINVAL;
+    const CombineBwdArgs a = {grad_out, rows, pair_row, topk_w, sorted_token_ids, num_tokens_post_pad, grad_rows, grad_w,
+                              status, drop, p->T, p->topk, p->n_rows, p->H};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return p->dtype == MR_F32 ? combine_bwd_of<float>(a, st) : combine_bwd_of<__nv_bfloat16>(a, st);
+}
+
+}  // extern "C"
