@@ -13,18 +13,37 @@
 namespace mr {
 namespace {
 
+__device__ __forceinline__ float rcp_hw(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // act(g) and act'(g) in fp32. The sigmoid is a hardware exponential (of the two-part product, exp_value) and
-// reciprocal: 1 to 2 units of the last place. Phi(g) = erfc(-g / sqrt 2) / 2 keeps its bits for g below zero.
+// reciprocal: 1 to 2 units of the last place. Phi(-a) = exp(-a^2 / 2) R(s), s = a / (4 + a): R, half the scaled
+// complementary error function of a / sqrt 2, is smooth in s, and a polynomial of degree 9 fitted here by least squares
+// that are weighted again until the errors level (Lawson's method) is within 2^-26 of it, relative, for a up to 14,
+// where the exponential is 0. Near a = 0 an error of s counts little, and behind it R's grows no faster than the
+// exponential's, so Phi keeps its bits for g below zero. Phi(a) = 1 - Phi(-a).
 template <int ACT, bool GRAD>
 __device__ __forceinline__ float gate(float g, float& da)
 {
     if constexpr (ACT == MR_SILU) {
-        const float s = __fdividef(1.0f, 1.0f + exp_value(-g)), a = g * s;
+        const float s = rcp_hw(1.0f + exp_value(-g)), a = g * s;
         if constexpr (GRAD) da = fmaf(a, 1.0f - s, s);
         return a;
     } else {
-        const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
-        if constexpr (GRAD) da = fmaf(g, 0.39894228040143268f * exp_value(-0.5f * g * g), cdf);
+        constexpr float kR[] = {0.5f, -1.5957679748535156f, 2.4041967391967773f, -2.1061601638793945f, 0.8699361681938171f,
+                                0.10994171351194382f, -0.2098998725414276f, -0.04766450077295303f, 0.10934294760227203f,
+                                -0.03394665941596031f};
+        const float m = fminf(fabsf(g), 14.0f), q = 0.25f * m, s = q * rcp_hw(1.0f + q), e = exp_value(-0.5f * g * g);
+        float t = kR[9];
+#pragma unroll
+        for (int i = 8; i >= 0; --i) t = fmaf(t, s, kR[i]);
+        t *= e;
+        const float cdf = g > 0.0f ? 1.0f - t : t;
+        if constexpr (GRAD) da = fmaf(g, 0.39894228040143268f * e, cdf);
         return g * cdf;
     }
 }
@@ -103,8 +122,14 @@ struct DropoutArgs {
     int T, W, wc;
 };
 
-template <typename T, bool VEC, bool DROP>
-__global__ void __launch_bounds__(kRowsThreads) k_dropout(const __grid_constant__ DropoutArgs a)
+// Without a residual a warp has one load of 512 bytes in flight beside the generator's chain of dependent products:
+// what counts is the number of warps, so these kernels keep to 32 registers (16384 x 4096 in bf16: 47 us, 5.7 TB/s,
+// against 51 with 36 to 40; two rows a warp or the next row's load ahead take more registers and 56 to 62). With a
+// residual there are twice the loads a warp, and 40 registers are better (16384 x 2048: 31.5 us, 6.4 TB/s, against 33).
+constexpr int dropout_ctas(bool few_registers) { return few_registers ? 8 : 0; }  // 0: the compiler's choice
+
+template <typename T, bool VEC, bool DROP, bool RES>
+__global__ void __launch_bounds__(kRowsThreads, dropout_ctas(VEC && !RES)) k_dropout(const __grid_constant__ DropoutArgs a)
 {
     pdl_trigger_small();
     pdl_wait();
@@ -118,12 +143,12 @@ __global__ void __launch_bounds__(kRowsThreads) k_dropout(const __grid_constant_
          t += static_cast<long long>(gridDim.x) * tall) {
         Pack<T> p, q;
         load_span<VEC>(static_cast<const T*>(a.x) + t * a.W, c0, a.W, lane, p);
-        if (a.residual) load_span<VEC>(static_cast<const T*>(a.residual) + t * a.W, c0, a.W, lane, q);
+        if constexpr (RES) load_span<VEC>(static_cast<const T*>(a.residual) + t * a.W, c0, a.W, lane, q);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = p.get(e);
         if constexpr (DROP) drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(t), c0, lane, v);
-        if (a.residual) {
+        if constexpr (RES) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += q.get(e);
         }
@@ -140,7 +165,7 @@ int launch_spans(void (*kernel)(Args), Args a, long long rows, cudaStream_t st)
 {
     const int spans = spans_of(a.W);
     a.wc = warps_across(spans);
-    const dim3 grid = span_grid(reinterpret_cast<const void*>(kernel), rows, spans, a.wc);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(kernel), rows, spans, a.wc, 0);
     if (grid.x < 1) return MR_ECUDA;
     return launch_kernel(kernel, grid, dim3(kRowsThreads), 0, st, 0, a) == cudaSuccess ? MR_OK : MR_ECUDA;
 }
@@ -166,14 +191,22 @@ int act_call(const ActArgs& a, int act, int dtype, cudaStream_t st)
     return dtype == MR_F32 ? act_of<float, MR_GELU, BWD>(a, st) : act_of<B, MR_GELU, BWD>(a, st);
 }
 
+template <typename T, bool VEC>
+int dropout_vec(const DropoutArgs& a, cudaStream_t st)
+{
+    if (a.drop.cut)
+        return a.residual ? launch_spans(k_dropout<T, VEC, true, true>, a, a.T, st)
+                          : launch_spans(k_dropout<T, VEC, true, false>, a, a.T, st);
+    return a.residual ? launch_spans(k_dropout<T, VEC, false, true>, a, a.T, st)
+                      : launch_spans(k_dropout<T, VEC, false, false>, a, a.T, st);
+}
+
 template <typename T>
 int dropout_of(const DropoutArgs& a, cudaStream_t st)
 {
     const size_t n = kVecBytes<T>;
     const bool vec = a.W % 8 == 0 && at_multiple(a.x, n) && at_multiple(a.residual, n) && at_multiple(a.y, n);
-    if (a.drop.cut)
-        return vec ? launch_spans(k_dropout<T, true, true>, a, a.T, st) : launch_spans(k_dropout<T, false, true>, a, a.T, st);
-    return vec ? launch_spans(k_dropout<T, true, false>, a, a.T, st) : launch_spans(k_dropout<T, false, false>, a, a.T, st);
+    return vec ? dropout_vec<T, true>(a, st) : dropout_vec<T, false>(a, st);
 }
 
 int check_act(const mr_act_params* p)

@@ -5,6 +5,7 @@
 //   g = m[t] grad_out[t]:  grad_rows[r(t,j)] = w[t,j] g,  grad_w[t,j] = <g, rows[r(t,j)]>
 // All are bound by memory. A token's slots are summed in slot order in fp32 and rounded once: no atomics, the same
 // bits each time.
+#include <algorithm>
 #include <climits>
 
 #include "rows.cuh"
@@ -27,7 +28,10 @@ struct PermuteArgs {
     int wc;
 };
 
-// A warp copies 32 * N words of a row, all of its loads in flight before the first store.
+// A warp copies 32 * N words of a row, all of its loads in flight before the first store, the next row's id behind them.
+// Bound by the writes: rows are evicted first, which leaves L2 to x, whose rows are read topk times (8192 tokens, 64
+// experts, topk 8, 2048 columns in bf16: 62 us instead of 68), and handed out in six waves of CTAs, since memory serves
+// some SMs faster than others (51 us, 6.1 TB/s; each SM an equal share 62, a CTA for every few rows 61).
 template <typename Word, int N>
 __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant__ PermuteArgs a)
 {
@@ -49,9 +53,12 @@ __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant_
         rows = a.n_rows;
     }
     if (first >= a.words) return;
-    for (long long r = static_cast<long long>(blockIdx.x) * tall + (warp >> a.wc); r < rows;
-         r += static_cast<long long>(gridDim.x) * tall) {
-        const int id = __ldcg(a.ids + r);
+    const long long step = static_cast<long long>(gridDim.x) * tall;
+    long long r = static_cast<long long>(blockIdx.x) * tall + (warp >> a.wc);
+    int next = r < rows ? __ldcg(a.ids + r) : 0;
+    for (; r < rows; r += step) {
+        const int id = next;
+        if (r + step < rows) next = __ldcg(a.ids + r + step);
         const bool real = id >= 0 && id < a.P;
         Word v[N];
         const Word* src = static_cast<const Word*>(a.x) + static_cast<long long>(real ? id / a.topk : 0) * a.words;
@@ -65,7 +72,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant_
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int c = first + 32 * i + lane;
-            if (c < a.words) dst[c] = v[i];
+            if (c < a.words) __stcs(dst + c, v[i]);
         }
         if (first == 0 && lane == 0) {
             if (real) a.pair_row[id] = static_cast<int32_t>(r);
@@ -160,36 +167,43 @@ struct CombineBwdArgs {
     float* grad_w;
     int32_t* status;
     DropArgs drop;
-    int T, topk, n_rows, W;
+    int T, topk, n_rows, W, wc, pad_span;
 };
 
+// Zeroes the padding rows among the sorted positions from u * pad_span on, pad_span of them (at most 32).
+template <bool VEC, typename T>
+__device__ __forceinline__ void zero_padding(const CombineBwdArgs& a, long long u, int lane)
+{
+    const long long first = u * a.pad_span;
+    bool pad = false;
+    if (lane < a.pad_span && first + lane < min(__ldcg(a.npp), a.n_rows)) {
+        const int id = __ldcg(a.ids + first + lane);
+        pad = id < 0 || id >= static_cast<long long>(a.T) * a.topk;
+    }
+    for (unsigned m = __ballot_sync(kFull, pad); m; m &= m - 1) {
+        T* row = static_cast<T*>(a.grad_rows) + (first + __ffs(m) - 1) * a.W;
+        const Pack<T> zero = {};
+        for (int c0 = 0; c0 < a.W; c0 += kSpan) store_span<VEC>(row, c0, a.W, lane, zero);
+    }
+}
+
 // A warp per pair, a token's pairs side by side so that its gradient comes from L2 or L1 after the first; behind the
-// pairs a warp per 32 sorted positions, which zeroes the padding rows among them.
+// pairs the padding rows. The kernel without dropout: 8192 tokens, topk 8, 2048 columns in bf16 take 93 us (6.2 TB/s),
+// 98 with a token's pairs in one warp.
 template <typename T, bool VEC, bool DROP>
-__global__ void __launch_bounds__(kRowsThreads) k_combine_bwd(const __grid_constant__ CombineBwdArgs a)
+__global__ void __launch_bounds__(kRowsThreads) k_combine_bwd_pairs(const __grid_constant__ CombineBwdArgs a)
 {
     constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
     pdl_trigger_small();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const long long P = static_cast<long long>(a.T) * a.topk, warps = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
-    const long long units = P + (a.n_rows + 31) / 32;
+    const long long units = P + (a.n_rows + a.pad_span - 1) / a.pad_span;
     DropState ds;
     if constexpr (DROP) ds = drop_state(a.drop);
     for (long long u = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
         if (u >= P) {
-            const long long pos = (u - P) * 32 + lane;
-            const int rows = min(__ldcg(a.npp), a.n_rows);
-            bool pad = false;
-            if (pos < rows) {
-                const int id = __ldcg(a.ids + pos);
-                pad = id < 0 || id >= P;
-            }
-            for (unsigned m = __ballot_sync(kFull, pad); m; m &= m - 1) {
-                T* row = static_cast<T*>(a.grad_rows) + (pos - lane + __ffs(m) - 1) * a.W;
-                const Pack<T> zero = {};
-                for (int c0 = 0; c0 < a.W; c0 += kSpan) store_span<VEC>(row, c0, a.W, lane, zero);
-            }
+            zero_padding<VEC, T>(a, u - P, lane);
             continue;
         }
         int r = __ldcg(a.pair_row + u);
@@ -235,6 +249,89 @@ __global__ void __launch_bounds__(kRowsThreads) k_combine_bwd(const __grid_const
     }
 }
 
+// With dropout: 2^wc warps share a token. Each takes every 2^wc-th span of its gradient, makes the factors there once
+// for kTokenRows of the token's rows at a time, and adds their dot products over its lanes, then the warps' in their
+// order. 8192 tokens, topk 4, 4096 columns in bf16: 97 us (6.4 TB/s) against 113 with the factors made for every pair;
+// eight rows at a time take 110, eight warps a token 100, one 106. Behind the tokens the padding rows.
+constexpr int kTokenRows = 4;
+constexpr int kTokenWarpsLog2 = 2;
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRowsThreads) k_combine_bwd_tokens(const __grid_constant__ CombineBwdArgs a)
+{
+    constexpr int KB = kTokenRows;
+    __shared__ float part[2][kRowsThreads / 32][KB];
+    pdl_trigger_small();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int across = 1 << a.wc, tall = (kRowsThreads / 32) >> a.wc, mine = warp & (across - 1);
+    const DropState ds = drop_state(a.drop);
+    int turn = 0;
+    for (long long t0 = static_cast<long long>(blockIdx.x) * tall; t0 < a.T; t0 += static_cast<long long>(gridDim.x) * tall) {
+        const long long t = t0 + (warp >> a.wc);
+        const T* g = static_cast<const T*>(a.grad_out) + t * a.W;
+        for (int j0 = 0; j0 < a.topk; j0 += KB) {
+            int r = -1;
+            float w = 0.0f;
+            if (t < a.T && lane < KB && j0 + lane < a.topk) {
+                r = __ldcg(a.pair_row + t * a.topk + j0 + lane);
+                w = __ldcg(a.w + t * a.topk + j0 + lane);
+                if (r < -1 || r >= a.n_rows) {
+                    if (mine == 0) report_status(a.status, kStatusRange);
+                    r = -1;
+                }
+            }
+            const bool any = __any_sync(kFull, r >= 0);
+            float dot[KB] = {};
+            for (int c0 = mine * kSpan; any && c0 < a.W; c0 += across * kSpan) {
+                Pack<T> pg, pr[KB];
+                load_span<VEC>(g, c0, a.W, lane, pg, j0 + KB >= a.topk);
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+                    const int rj = __shfl_sync(kFull, r, j);
+                    if (rj >= 0) load_span<VEC>(static_cast<const T*>(a.rows) + static_cast<long long>(rj) * a.W, c0, a.W, lane, pr[j]);
+                }
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = pg.get(e);
+                drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(t), c0, lane, v);
+#pragma unroll
+                for (int j = 0; j < KB; ++j) {
+                    const int rj = __shfl_sync(kFull, r, j);
+                    const float wj = __shfl_sync(kFull, w, j);
+                    if (rj < 0) continue;
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dot[j] = fmaf(v[e], pr[j].get(e), dot[j]);
+                        o[e] = v[e] * wj;
+                    }
+                    Pack<T> q;
+                    q.set(o);
+                    store_span<VEC>(static_cast<T*>(a.grad_rows) + static_cast<long long>(rj) * a.W, c0, a.W, lane, q);
+                }
+            }
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                const float s = warp_sum(dot[j]);
+                if (lane == j) sum = s;
+            }
+            if (across > 1) {
+                if (lane < KB) part[turn][warp][lane] = sum;
+                __syncthreads();
+                if (mine == 0 && lane < KB)
+                    for (int i = 1; i < across; ++i) sum += part[turn][warp + i][lane];
+                turn ^= 1;
+            }
+            if (mine == 0 && t < a.T && lane < KB && j0 + lane < a.topk) a.grad_w[t * a.topk + j0 + lane] = sum;
+        }
+    }
+    const long long units = (a.n_rows + a.pad_span - 1) / a.pad_span, warps = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
+    for (long long u = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + warp; u < units; u += warps)
+        zero_padding<VEC, T>(a, u, lane);
+}
+
 // ---- host --------------------------------------------------------------------
 
 int check_rows(const mr_rows_params* p)
@@ -252,7 +349,7 @@ int permute(PermuteArgs a, size_t row_bytes, cudaStream_t st)
     a.words = static_cast<int>(row_bytes / sizeof(Word));
     const int spans = (a.words + 32 * N - 1) / (32 * N);
     a.wc = warps_across(spans);
-    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_permute<Word, N>), a.n_rows, spans, a.wc);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_permute<Word, N>), a.n_rows, spans, a.wc, 6);
     if (grid.x < 1) return MR_ECUDA;
     const int e = launch_kernel(k_permute<Word, N>, grid, dim3(kRowsThreads), 0, st, 0, a);
     return e == cudaSuccess ? MR_OK : MR_ECUDA;
@@ -263,7 +360,7 @@ int combine(CombineArgs a, cudaStream_t st)
 {
     const int spans = spans_of(a.W);
     a.wc = warps_across(spans);
-    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_combine<T, VEC, DROP>), a.T, spans, a.wc);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_combine<T, VEC, DROP>), a.T, spans, a.wc, 0);
     if (grid.x < 1) return MR_ECUDA;
     const int e = launch_kernel(k_combine<T, VEC, DROP>, grid, dim3(kRowsThreads), 0, st, 0, a);
     return e == cudaSuccess ? MR_OK : MR_ECUDA;
@@ -279,13 +376,31 @@ int combine_of(const CombineArgs& a, cudaStream_t st)
 }
 
 template <typename T, bool VEC, bool DROP>
-int combine_bwd(const CombineBwdArgs& a, cudaStream_t st)
+int combine_bwd(CombineBwdArgs a, cudaStream_t st)
 {
-    const long long warps = static_cast<long long>(a.T) * a.topk + (a.n_rows + 31) / 32;
-    const int g = persistent_grid(reinterpret_cast<const void*>(k_combine_bwd<T, VEC, DROP>), kRowsThreads, 0,
-                                  (warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32), true);
+    const int warps = kRowsThreads / 32;
+    const long long pairs = static_cast<long long>(a.T) * a.topk;
+    // a warp's share of the padding: small layouts are mostly padding and want all SMs for it (64 tokens, 256 experts,
+    // blocks of 16: 5.4 us against 16 with 32 rows a warp), in large ones looking for it is what costs
+    a.pad_span = a.n_rows <= 32768 ? 4 : 32;
+    const long long pads = (a.n_rows + a.pad_span - 1) / a.pad_span;
+    if constexpr (DROP) {
+        // T=1024 H=2048: topk 4 12.3 us against 12.8 pair by pair, topk 1 10.1 against 7.6; T=512: topk 4 9.5 against 8.3,
+        // topk 8 15.0 against 14.6
+        if (a.topk >= 3 && pairs >= 4096) {
+            const auto kernel = k_combine_bwd_tokens<T, VEC>;
+            a.wc = std::min(warps_across(spans_of(a.W)), kTokenWarpsLog2);
+            const int tall = warps >> a.wc;
+            const long long g = dynamic_grid(reinterpret_cast<const void*>(kernel), (a.T + tall - 1) / tall, 6);
+            if (g < 1) return MR_ECUDA;
+            const int e = launch_kernel(kernel, dim3(static_cast<unsigned>(g)), dim3(kRowsThreads), 0, st, 0, a);
+            return e == cudaSuccess ? MR_OK : MR_ECUDA;
+        }
+    }
+    const auto kernel = k_combine_bwd_pairs<T, VEC, DROP>;
+    const int g = persistent_grid(reinterpret_cast<const void*>(kernel), kRowsThreads, 0, (pairs + pads + warps - 1) / warps, true);
     if (g < 1) return MR_ECUDA;
-    const int e = launch_kernel(k_combine_bwd<T, VEC, DROP>, dim3(g), dim3(kRowsThreads), 0, st, 0, a);
+    const int e = launch_kernel(kernel, dim3(g), dim3(kRowsThreads), 0, st, 0, a);
     return e == cudaSuccess ? MR_OK : MR_ECUDA;
 }
 
@@ -344,7 +459,7 @@ int moe_permute_bwd(const mr_rows_params* p, const void* grad_rows, const int32_
     if ((p->n_rows > 0 && !grad_rows) || !pair_row || !grad_x) return MR_EINVAL;
     if (!at_multiple(grad_rows, size) || !at_multiple(grad_x, size) || !at_multiple(pair_row, 4) || !at_multiple(status, 4))
         return MR_EINVAL;
-    return combine_call(*p, grad_rows, pair_row, nullptr, nullptr, DropArgs{nullptr, 0, 1.0f}, grad_x, status,
+    return combine_call(*p, grad_rows, pair_row, nullptr, nullptr, DropArgs{}, grad_x, status,
                         reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -382,7 +497,7 @@ int moe_combine_bwd(const mr_rows_params* p, const void* grad_out, const void* r
         !at_multiple(grad_w, 4) || !at_multiple(status, 4))
         return MR_EINVAL;
     const CombineBwdArgs a = {grad_out, rows, pair_row, topk_w, sorted_token_ids, num_tokens_post_pad, grad_rows, grad_w,
-                              status, drop, p->T, p->topk, p->n_rows, p->H};
+                              status, drop, p->T, p->topk, p->n_rows, p->H, 0, 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return p->dtype == MR_F32 ? combine_bwd_of<float>(a, st) : combine_bwd_of<__nv_bfloat16>(a, st);
 }

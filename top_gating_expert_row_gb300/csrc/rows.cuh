@@ -2,6 +2,7 @@
 // 256 columns of one row, eight to a lane.
 #pragma once
 
+#include <algorithm>
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -141,7 +142,8 @@ __device__ __forceinline__ void store_span(T* row, int c0, int W, int lane, cons
 // ---------------------------------------------------------------------------
 struct DropArgs {
     const unsigned long long* rng;  // {seed, offset}
-    uint32_t cut;                   // 1..65536
+    uint32_t cut;                   // 1..65536 (0: nothing is dropped, and the kernels without dropout run)
+    uint32_t above;                 // cut * 2^16 - 1: 16 bits on top of a word keep their element iff the word is above
     float scale;                    // 0 where nothing is kept
 };
 
@@ -183,17 +185,14 @@ __device__ __forceinline__ void drop_span(const DropArgs& d, const DropState& s,
     if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t bits = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
-            v[i] = bits >= d.cut ? v[i] * d.scale : 0.0f;
+            const bool kept = ((i & 1) ? w[i >> 1] : w[i >> 1] << 16) > d.above;
+            v[i] = kept ? v[i] * d.scale : 0.0f;
         }
     } else {
         // lane l made block c0 / 8 + l: its eight bits go to the lanes that hold these columns
         uint32_t keep = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t bits = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
-            keep |= (bits >= d.cut ? 1u : 0u) << i;
-        }
+        for (int i = 0; i < 8; ++i) keep |= (((i & 1) ? w[i >> 1] : w[i >> 1] << 16) > d.above ? 1u : 0u) << i;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t k = __shfl_sync(kFull, keep, 4 * i + (lane >> 3));
@@ -213,16 +212,28 @@ inline int warps_across(int spans)
     return 0;
 }
 
+// CTAs for `units` of work. waves 0: no more than are resident, each with the same number of units in turn. Otherwise,
+// where there are units for it, up to about `waves` times as many, handed out as others end, so that SMs that memory
+// serves faster take more. A CTA's start costs too (about 3.6 ns of the GPU's time): which is better differs from kernel
+// to kernel, as measured there. -1 on an error.
+inline long long dynamic_grid(const void* kernel, long long units, int waves)
+{
+    const int resident = persistent_grid(kernel, kRowsThreads, 0, units, false);
+    if (resident < 1) return resident;
+    if (waves == 0 || units < 3ll * resident) return persistent_grid(kernel, kRowsThreads, 0, units, true);
+    const long long each = std::max<long long>(1, units / (static_cast<long long>(resident) * waves));
+    return (units + each - 1) / each;
+}
+
 // A grid of (row groups, span groups) for CTAs that take 2^wc spans of 8 >> wc rows at a time; x is 0 on an error.
-inline dim3 span_grid(const void* kernel, long long rows, int spans, int wc)
+inline dim3 span_grid(const void* kernel, long long rows, int spans, int wc, int waves)
 {
     const int tall = (kRowsThreads / 32) >> wc;
     const unsigned y = static_cast<unsigned>((spans + (1 << wc) - 1) >> wc);
     const long long need = rows > tall ? (rows + tall - 1) / tall : 1;
-    const int g = persistent_grid(kernel, kRowsThreads, 0, need * y, true);
+    const long long g = dynamic_grid(kernel, need * y, waves);
     if (g < 1) return dim3(0);
-    const long long x = (g + y - 1) / y;
-    return dim3(static_cast<unsigned>(x < need ? x : need), y);
+    return dim3(static_cast<unsigned>(std::min((g + y - 1) / y, need)), y);
 }
 
 // Host side of dropout's arguments: p in [0, 1] and, where it drops anything, the generator's state. False if either
@@ -231,6 +242,7 @@ inline bool drop_args(float p, const void* rng, DropArgs& d)
 {
     if (!(p >= 0.0f && p <= 1.0f)) return false;
     d.cut = static_cast<uint32_t>(static_cast<double>(p) * 65536.0 + 0.5);
+    d.above = (d.cut << 16) - 1u;  // nothing is above where cut is 2^16
     d.scale = d.cut < 65536u ? static_cast<float>(65536.0 / (65536.0 - d.cut)) : 0.0f;
     d.rng = static_cast<const unsigned long long*>(rng);
     return d.cut == 0 || (rng && (reinterpret_cast<uintptr_t>(rng) & 7) == 0);
