@@ -26,25 +26,31 @@ __device__ __forceinline__ float rcp_hw(float x)
 // that are weighted again until the errors level (Lawson's method) is within 2^-26 of it, relative, for a up to 14,
 // where the exponential is 0. Near a = 0 an error of s counts little, and behind it R's grows no faster than the
 // exponential's, so Phi keeps its bits for g below zero. Phi(a) = 1 - Phi(-a).
+// Two values at a time, in packed instructions where there are any (each half rounds as the single one does).
 template <int ACT, bool GRAD>
-__device__ __forceinline__ float gate(float g, float& da)
+__device__ __forceinline__ float2 gate(float2 g, float2& da)
 {
+    const float2 one = make_float2(1.0f, 1.0f);
     if constexpr (ACT == MR_SILU) {
-        const float s = rcp_hw(1.0f + exp_value(-g)), a = g * s;
-        if constexpr (GRAD) da = fmaf(a, 1.0f - s, s);
+        const float2 d = __fadd2_rn(one, exp_value2(make_float2(-g.x, -g.y)));
+        const float2 s = make_float2(rcp_hw(d.x), rcp_hw(d.y)), a = __fmul2_rn(g, s);
+        if constexpr (GRAD) da = __ffma2_rn(a, __fadd2_rn(one, make_float2(-s.x, -s.y)), s);
         return a;
     } else {
         constexpr float kR[] = {0.5f, -1.5957679748535156f, 2.4041967391967773f, -2.1061601638793945f, 0.8699361681938171f,
                                 0.10994171351194382f, -0.2098998725414276f, -0.04766450077295303f, 0.10934294760227203f,
                                 -0.03394665941596031f};
-        const float m = fminf(fabsf(g), 14.0f), q = 0.25f * m, s = q * rcp_hw(1.0f + q), e = exp_value(-0.5f * g * g);
-        float t = kR[9];
+        auto both = [](float v) { return make_float2(v, v); };
+        const float2 q = __fmul2_rn(both(0.25f), make_float2(fminf(fabsf(g.x), 14.0f), fminf(fabsf(g.y), 14.0f)));
+        const float2 d = __fadd2_rn(one, q), s = __fmul2_rn(q, make_float2(rcp_hw(d.x), rcp_hw(d.y)));
+        const float2 e = exp_value2(__fmul2_rn(__fmul2_rn(both(-0.5f), g), g));
+        float2 t = both(kR[9]);
 #pragma unroll
-        for (int i = 8; i >= 0; --i) t = fmaf(t, s, kR[i]);
-        t *= e;
-        const float cdf = g > 0.0f ? 1.0f - t : t;
-        if constexpr (GRAD) da = fmaf(g, 0.39894228040143268f * e, cdf);
-        return g * cdf;
+        for (int i = 8; i >= 0; --i) t = __ffma2_rn(t, s, both(kR[i]));
+        t = __fmul2_rn(t, e);
+        const float2 cdf = make_float2(g.x > 0.0f ? 1.0f - t.x : t.x, g.y > 0.0f ? 1.0f - t.y : t.y);
+        if constexpr (GRAD) da = __ffma2_rn(g, __fmul2_rn(both(0.39894228040143268f), e), cdf);
+        return __fmul2_rn(g, cdf);
     }
 }
 
@@ -78,9 +84,14 @@ __global__ void __launch_bounds__(kRowsThreads) k_act(const __grid_constant__ Ac
         load_span<VEC>(gu + a.W, c0, a.W, lane, pu);
         if constexpr (BWD) load_span<VEC>(static_cast<const T*>(a.grad_h) + r * a.W, c0, a.W, lane, pd);
         if constexpr (!BWD) {
-            float v[8], da;
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = gate<ACT, false>(pg.get(e), da) * pu.get(e);
+            for (int e = 0; e < 8; e += 2) {
+                float2 da;
+                const float2 act = gate<ACT, false>(make_float2(pg.get(e), pg.get(e + 1)), da);
+                v[e] = act.x * pu.get(e);
+                v[e + 1] = act.y * pu.get(e + 1);
+            }
             if constexpr (DROP) drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(r), c0, lane, v);
             Pack<T> q;
             q.set(v);
@@ -91,14 +102,19 @@ __global__ void __launch_bounds__(kRowsThreads) k_act(const __grid_constant__ Ac
             for (int e = 0; e < 8; ++e) m[e] = 1.0f;
             if constexpr (DROP) drop_span<VEC>(a.drop, ds, static_cast<uint32_t>(r), c0, lane, m);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float da;
-                const float act = gate<ACT, true>(pg.get(e), da), u = pu.get(e);
-                // a dropped element is 0 whatever it held
-                const float d = !DROP || m[e] != 0.0f ? m[e] * pd.get(e) : 0.0f;
-                v[e] = !DROP || m[e] != 0.0f ? m[e] * act * u : 0.0f;
-                gq[e] = !DROP || m[e] != 0.0f ? d * act : 0.0f;
-                gg[e] = !DROP || m[e] != 0.0f ? d * u * da : 0.0f;
+            for (int e0 = 0; e0 < 8; e0 += 2) {
+                float2 da2;
+                const float2 act2 = gate<ACT, true>(make_float2(pg.get(e0), pg.get(e0 + 1)), da2);
+#pragma unroll
+                for (int e = e0; e < e0 + 2; ++e) {
+                    const float act = e == e0 ? act2.x : act2.y, da = e == e0 ? da2.x : da2.y, u = pu.get(e);
+                    // a dropped element is 0 whatever it held
+                    const bool kept = !DROP || m[e] != 0.0f;
+                    const float d = kept ? m[e] * pd.get(e) : 0.0f;
+                    v[e] = kept ? m[e] * act * u : 0.0f;
+                    gq[e] = kept ? d * act : 0.0f;
+                    gg[e] = kept ? d * u * da : 0.0f;
+                }
             }
             T* grad = static_cast<T*>(a.grad_gu) + r * 2 * a.W;
             Pack<T> q;

@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_combine_bwd_pairs(const __grid
                 Pack<T> pg[kBatch], pr[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    load_span<VEC>(row, c + i * kSpan, a.W, lane, pr[i]);
-                    load_span<VEC>(g, c + i * kSpan, a.W, lane, pg[i], false);
+                    load_span<VEC, false>(row, c + i * kSpan, a.W, lane, pr[i]);
+                    load_span<VEC, false>(g, c + i * kSpan, a.W, lane, pg[i], false);
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {

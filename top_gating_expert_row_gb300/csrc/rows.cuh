@@ -3,6 +3,8 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -85,8 +87,9 @@ __device__ __forceinline__ void store_vec(float* p, const Pack<float>& q)
 }
 
 // The lane's eight elements of the span at column c0 of a row of W; zeros past its end. once: read by this warp
-// alone (evicted first).
-template <bool VEC, typename T>
+// alone (evicted first). BRANCH: whole spans of unaligned rows without comparisons, at offsets that the loads hold
+// themselves; a kernel that asks for several spans in a row does without, the branches would hold its loads up.
+template <bool VEC, bool BRANCH = true, typename T>
 __device__ __forceinline__ void load_span(const T* row, int c0, int W, int lane, Pack<T>& q, bool once = true)
 {
     if constexpr (VEC) {
@@ -96,22 +99,24 @@ __device__ __forceinline__ void load_span(const T* row, int c0, int W, int lane,
 #pragma unroll
             for (int i = 0; i < static_cast<int>(sizeof(q.w) / 4); ++i) q.w[i] = 0u;
         }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + 32 * i + lane;
-            q.w[i] = c < W ? __float_as_uint(once ? __ldcs(row + c) : row[c]) : 0u;
-        }
     } else {
-        const unsigned short* p = reinterpret_cast<const unsigned short*>(row);
+        using E = std::conditional_t<sizeof(T) == 4, uint32_t, unsigned short>;
+        const E* p = reinterpret_cast<const E*>(row) + c0 + lane;
         uint32_t b[8];
+        if (BRANCH && c0 + kSpan <= W) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + 32 * i + lane;
-            b[i] = c < W ? (once ? __ldcs(p + c) : p[c]) : 0u;
+            for (int i = 0; i < 8; ++i) b[i] = once ? __ldcs(p + 32 * i) : p[32 * i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = c0 + 32 * i + lane < W ? (once ? __ldcs(p + 32 * i) : p[32 * i]) : 0u;
         }
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q.w[i] = b[2 * i] | b[2 * i + 1] << 16;
+            for (int i = 0; i < 8; ++i) q.w[i] = b[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q.w[i] = b[2 * i] | b[2 * i + 1] << 16;
+        }
     }
 }
 
@@ -121,12 +126,19 @@ __device__ __forceinline__ void store_span(T* row, int c0, int W, int lane, cons
     if constexpr (VEC) {
         if (c0 + 8 * lane < W) store_vec(row + c0 + 8 * lane, q);
     } else {
+        using E = std::conditional_t<sizeof(T) == 4, uint32_t, unsigned short>;
+        E* p = reinterpret_cast<E*>(row) + c0 + lane;
+        auto value = [&](int i) {
+            if constexpr (sizeof(T) == 4) return q.w[i];
+            else return static_cast<E>(q.w[i >> 1] >> (16 * (i & 1)));
+        };
+        if (c0 + kSpan <= W) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + 32 * i + lane;
-            if (c >= W) continue;
-            if constexpr (sizeof(T) == 4) row[c] = __uint_as_float(q.w[i]);
-            else reinterpret_cast<unsigned short*>(row)[c] = static_cast<unsigned short>(q.w[i >> 1] >> (16 * (i & 1)));
+            for (int i = 0; i < 8; ++i) p[32 * i] = value(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c0 + 32 * i + lane < W) p[32 * i] = value(i);
         }
     }
 }
