@@ -145,6 +145,23 @@ def test_combine(mr, size, dtype, p):
     assert torch.equal(again["grad_rows"][: s["n"]], buf[: s["n"]])
 
 
+MANY = [  # T, topk, E, H, block, dropped, shift: more pairs and rows than the GPU takes at a time
+    (1400, 3, 16, 257, 16, 0.2, 0),
+    (1030, 4, 64, 2304, 32, 0.0, 0),
+    (130, 33, 40, 264, 8, 0.1, 1),
+    (9000, 4, 32, 40, 16, 0.1, 0),
+    (2500, 9, 384, 64, 1, 0.0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("size", MANY, ids=str)
+def test_many_pairs(mr, size, dtype):
+    """The same checks where CTAs take several rows, and where a token's rows share its dropout factors."""
+    test_permute(mr, size, dtype)
+    test_combine(mr, size, dtype, 0.3)
+
+
 def gate_tolerance(g, kind):
     """Relative error of act(g), absolute error of act'(g), in 64 bits.
 
@@ -212,6 +229,18 @@ def test_expert_act(mr, size, dtype, kind, p):
     assert set(less) == {"grad_gu"} and torch.equal(less["grad_gu"][:m], out["grad_gu"][:m])
     if m == n:  # without a count: all rows
         assert torch.equal(mr.expert_act(put(gu), act=kind, p=p, rng=rng.cuda()), got)
+
+
+@pytest.mark.parametrize("kind", [0, 1], ids=["silu", "gelu"])
+def test_activation_everywhere(mr, kind):
+    """act and act' in fp32 at 2^19 gates from -16 to 16, up and grad_h being 1."""
+    g = torch.linspace(-16, 16, 1 << 19).view(512, 1024)
+    gu = torch.cat([g, torch.ones_like(g)], 1)
+    a, da = ref.act(g.double(), kind)
+    ta, tda = gate_tolerance(g.double(), kind)
+    check(mr.expert_act(gu.cuda(), act=kind), a, ta, "h")
+    out = mr.expert_act_bwd(torch.ones_like(g).cuda(), gu.cuda(), act=kind)
+    check(out["grad_gu"], torch.cat([da, a], 1), torch.cat([tda, ta], 1), "grad_gu")
 
 
 @pytest.mark.parametrize("p", [0.0, 2.0 ** -18, 0.1, 0.999, 1.0])
