@@ -791,11 +791,17 @@ def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = N
 
 
 def _explicit_grad(bwd: str, *tensors) -> None:
-    if not torch.is_grad_enabled():
-        return
     for t in tensors:
-        if t is not None and t.requires_grad:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"gradients are computed by {bwd}(): call this under torch.no_grad(), or detach its inputs")
+
+
+def _here(device, stream) -> Optional[int]:
+    """The current stream's handle where the call needs nothing else than that: no stream named, the tensors' device
+    current. Otherwise None, and the call repeats itself under _launch()."""
+    if stream is None and device.type == "cuda" and torch._C._cuda_getDevice() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
 
 _ROW_DTYPES = {torch.float32: MR_F32, torch.bfloat16: MR_BF16}
@@ -809,12 +815,12 @@ def _row_dtype(what: str, t: torch.Tensor) -> int:
 
 
 def _check_rng(p: float, rng: Optional[torch.Tensor], device) -> Optional[int]:
+    if p == 0.0:
+        return None  # nothing is dropped, rng is not read
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must be in [0, 1], got {p}")
     if rng is None:
-        if p > 0.0:
-            raise ValueError("dropout needs rng, an int64 tensor {seed, offset}")
-        return None
+        raise ValueError("dropout needs rng, an int64 tensor {seed, offset}")
     _check("rng", rng, (2,), torch.int64, device)
     return rng.data_ptr()
 
@@ -835,10 +841,16 @@ def _act_plan(n_rows, I, act, dtype):
 
 
 def _check_pairs(name: str, t: torch.Tensor, device):
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} is [T, topk]")
-    _check(name, t, t.shape, torch.int32, device)
-    return t.shape
+    _check(name, t, shape, torch.int32, device)
+    return shape
+
+
+def _check_contiguous(what: str, t: torch.Tensor) -> None:
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
 
 
 def permute(x: torch.Tensor, topk_idx: torch.Tensor, E_tot: int, sorted_token_ids: torch.Tensor,
@@ -852,30 +864,34 @@ def permute(x: torch.Tensor, topk_idx: torch.Tensor, E_tot: int, sorted_token_id
         raise ValueError("x is [T, H], sorted_token_ids [n_rows]")
     (T, H), n, dev = x.shape, sorted_token_ids.shape[0], x.device
     code = _row_dtype("x", x)
-    _check("x", x, (T, H), x.dtype, dev)
-    k = _check_pairs("topk_idx", topk_idx, dev)[1]
-    _check("topk_idx", topk_idx, (T, k), torch.int32, dev)
+    _check_contiguous("x", x)
+    P, k = _check_pairs("topk_idx", topk_idx, dev)
+    if P != T:
+        raise ValueError(f"topk_idx must have shape {(T, k)}, got {(P, k)}")
     _check("sorted_token_ids", sorted_token_ids, (n,), torch.int32, dev)
     _check("num_tokens_post_pad", num_tokens_post_pad, (1,), torch.int32, dev)
     _check_buffer("rows", rows, (n, H), x.dtype, dev)
     st = _check_status(status, dev)
-    with _launch(dev, stream) as raw:
-        if rows is None:
-            rows = torch.empty(n, H, dtype=x.dtype, device=dev)
-        pair_row = torch.empty(T, k, dtype=torch.int32, device=dev)
-        _ok(_lib.moe_permute_fwd(_rows_plan(T, H, k, n, code), E_tot, x.data_ptr(), topk_idx.data_ptr(),
-                                 sorted_token_ids.data_ptr(), num_tokens_post_pad.data_ptr(), rows.data_ptr(),
-                                 pair_row.data_ptr(), st, raw), "moe_permute_fwd")
-    return dict(rows=rows, pair_row=pair_row)
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return permute(x, topk_idx, E_tot, sorted_token_ids, num_tokens_post_pad, rows, status)
+    out = torch.empty(n, H, dtype=x.dtype, device=dev) if rows is None else rows
+    pair_row = torch.empty(T, k, dtype=torch.int32, device=dev)
+    _ok(_lib.moe_permute_fwd(_rows_plan(T, H, k, n, code), E_tot, x.data_ptr(), topk_idx.data_ptr(),
+                             sorted_token_ids.data_ptr(), num_tokens_post_pad.data_ptr(), out.data_ptr(),
+                             pair_row.data_ptr(), st, raw), "moe_permute_fwd")
+    return dict(rows=out, pair_row=pair_row)
 
 
 def _rows_and_pairs(what: str, rows: torch.Tensor, pair_row: torch.Tensor):
-    if rows.dim() != 2:
+    shape = rows.shape
+    if len(shape) != 2:
         raise ValueError(f"{what} is [n_rows, H]")
     dev, code = rows.device, _row_dtype(what, rows)
-    _check(what, rows, rows.shape, rows.dtype, dev)
+    _check_contiguous(what, rows)
     T, k = _check_pairs("pair_row", pair_row, dev)
-    return T, k, rows.shape[0], rows.shape[1], dev, code
+    return T, k, shape[0], shape[1], dev, code
 
 
 def permute_bwd(grad_rows: torch.Tensor, pair_row: torch.Tensor, status: Optional[torch.Tensor] = None,
@@ -884,10 +900,13 @@ def permute_bwd(grad_rows: torch.Tensor, pair_row: torch.Tensor, status: Optiona
     _explicit_grad("permute", grad_rows)
     T, k, n, H, dev, code = _rows_and_pairs("grad_rows", grad_rows, pair_row)
     st = _check_status(status, dev)
-    with _launch(dev, stream) as raw:
-        gx = torch.empty(T, H, dtype=grad_rows.dtype, device=dev)
-        _ok(_lib.moe_permute_bwd(_rows_plan(T, H, k, n, code), grad_rows.data_ptr(), pair_row.data_ptr(),
-                                 gx.data_ptr(), st, raw), "moe_permute_bwd")
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return permute_bwd(grad_rows, pair_row, status)
+    gx = torch.empty(T, H, dtype=grad_rows.dtype, device=dev)
+    _ok(_lib.moe_permute_bwd(_rows_plan(T, H, k, n, code), grad_rows.data_ptr(), pair_row.data_ptr(),
+                             gx.data_ptr(), st, raw), "moe_permute_bwd")
     return gx
 
 
@@ -895,18 +914,22 @@ def combine(rows: torch.Tensor, pair_row: torch.Tensor, topk_w: torch.Tensor, re
             p: float = 0.0, rng: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
             stream=None) -> torch.Tensor:
     """moe_combine_fwd: out [T, H] = residual + dropout(the sum of each token's rows by topk_w [T, topk], fp32). rng
-    (int64 {seed, offset} on the device) says which elements dropout with probability p takes."""
+    (int64 {seed, offset} on the device) says which elements dropout with probability p takes; with p = 0 it is not
+    looked at."""
     _explicit_grad("combine_bwd", rows, topk_w, residual)
     T, k, n, H, dev, code = _rows_and_pairs("rows", rows, pair_row)
     _check("topk_w", topk_w, (T, k), torch.float32, dev)
     if residual is not None:
         _check("residual", residual, (T, H), rows.dtype, dev)
     r, st = _check_rng(p, rng, dev), _check_status(status, dev)
-    with _launch(dev, stream) as raw:
-        out = torch.empty(T, H, dtype=rows.dtype, device=dev)
-        _ok(_lib.moe_combine_fwd(_rows_plan(T, H, k, n, code), rows.data_ptr(), pair_row.data_ptr(), topk_w.data_ptr(),
-                                 None if residual is None else residual.data_ptr(), p, r, out.data_ptr(), st, raw),
-            "moe_combine_fwd")
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return combine(rows, pair_row, topk_w, residual, p, rng, status)
+    out = torch.empty(T, H, dtype=rows.dtype, device=dev)
+    _ok(_lib.moe_combine_fwd(_rows_plan(T, H, k, n, code), rows.data_ptr(), pair_row.data_ptr(), topk_w.data_ptr(),
+                             None if residual is None else residual.data_ptr(), p, r, out.data_ptr(), st, raw),
+        "moe_combine_fwd")
     return out
 
 
@@ -924,22 +947,25 @@ def combine_bwd(grad_out: torch.Tensor, rows: torch.Tensor, pair_row: torch.Tens
     _check("num_tokens_post_pad", num_tokens_post_pad, (1,), torch.int32, dev)
     _check_buffer("grad_rows", grad_rows, (n, H), rows.dtype, dev)
     r, st = _check_rng(p, rng, dev), _check_status(status, dev)
-    with _launch(dev, stream) as raw:
-        if grad_rows is None:
-            grad_rows = torch.empty_like(rows)
-        grad_w = torch.empty(T, k, dtype=torch.float32, device=dev)
-        _ok(_lib.moe_combine_bwd(_rows_plan(T, H, k, n, code), grad_out.data_ptr(), rows.data_ptr(),
-                                 pair_row.data_ptr(), topk_w.data_ptr(), sorted_token_ids.data_ptr(),
-                                 num_tokens_post_pad.data_ptr(), p, r, grad_rows.data_ptr(), grad_w.data_ptr(), st,
-                                 raw), "moe_combine_bwd")
-    return dict(grad_rows=grad_rows, grad_w=grad_w)
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return combine_bwd(grad_out, rows, pair_row, topk_w, sorted_token_ids, num_tokens_post_pad, p, rng, grad_rows,
+                               status)
+    grad = torch.empty_like(rows) if grad_rows is None else grad_rows
+    grad_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+    _ok(_lib.moe_combine_bwd(_rows_plan(T, H, k, n, code), grad_out.data_ptr(), rows.data_ptr(),
+                             pair_row.data_ptr(), topk_w.data_ptr(), sorted_token_ids.data_ptr(),
+                             num_tokens_post_pad.data_ptr(), p, r, grad.data_ptr(), grad_w.data_ptr(), st,
+                             raw), "moe_combine_bwd")
+    return dict(grad_rows=grad, grad_w=grad_w)
 
 
 def _check_gated(gu: torch.Tensor, num_rows):
     if gu.dim() != 2 or gu.shape[1] % 2:
         raise ValueError("gu is [n_rows, 2 * I]")
     dev, code = gu.device, _row_dtype("gu", gu)
-    _check("gu", gu, gu.shape, gu.dtype, dev)
+    _check_contiguous("gu", gu)
     if num_rows is not None:
         _check("num_rows", num_rows, (1,), torch.int32, dev)
     return gu.shape[0], gu.shape[1] // 2, dev, code, None if num_rows is None else num_rows.data_ptr()
@@ -953,12 +979,14 @@ def expert_act(gu: torch.Tensor, num_rows: Optional[torch.Tensor] = None, act: i
     n, I, dev, code, used = _check_gated(gu, num_rows)
     _check_buffer("h", h, (n, I), gu.dtype, dev)
     r = _check_rng(p, rng, dev)
-    with _launch(dev, stream) as raw:
-        if h is None:
-            h = torch.empty(n, I, dtype=gu.dtype, device=dev)
-        _ok(_lib.moe_expert_act_fwd(_act_plan(n, I, act, code), gu.data_ptr(), used, p, r, h.data_ptr(), raw),
-            "moe_expert_act_fwd")
-    return h
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return expert_act(gu, num_rows, act, p, rng, h)
+    out = torch.empty(n, I, dtype=gu.dtype, device=dev) if h is None else h
+    _ok(_lib.moe_expert_act_fwd(_act_plan(n, I, act, code), gu.data_ptr(), used, p, r, out.data_ptr(), raw),
+        "moe_expert_act_fwd")
+    return out
 
 
 def expert_act_bwd(grad_h: torch.Tensor, gu: torch.Tensor, num_rows: Optional[torch.Tensor] = None,
@@ -973,13 +1001,16 @@ def expert_act_bwd(grad_h: torch.Tensor, gu: torch.Tensor, num_rows: Optional[to
     _check_buffer("grad_gu", grad_gu, gu.shape, gu.dtype, dev)
     _check_buffer("h", h, (n, I), gu.dtype, dev)
     r = _check_rng(p, rng, dev)
-    with _launch(dev, stream) as raw:
-        out = dict(grad_gu=torch.empty_like(gu) if grad_gu is None else grad_gu)
-        if need_h:
-            out["h"] = torch.empty_like(grad_h) if h is None else h
-        _ok(_lib.moe_expert_act_bwd(_act_plan(n, I, act, code), grad_h.data_ptr(), gu.data_ptr(), used, p, r,
-                                    out["grad_gu"].data_ptr(), out["h"].data_ptr() if need_h else None, raw),
-            "moe_expert_act_bwd")
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return expert_act_bwd(grad_h, gu, num_rows, act, p, rng, grad_gu, h, need_h)
+    out = dict(grad_gu=torch.empty_like(gu) if grad_gu is None else grad_gu)
+    if need_h:
+        out["h"] = torch.empty_like(grad_h) if h is None else h
+    _ok(_lib.moe_expert_act_bwd(_act_plan(n, I, act, code), grad_h.data_ptr(), gu.data_ptr(), used, p, r,
+                                out["grad_gu"].data_ptr(), out["h"].data_ptr() if need_h else None, raw),
+        "moe_expert_act_bwd")
     return out
 
 
@@ -987,7 +1018,7 @@ def _check_hidden(what: str, x: torch.Tensor):
     if x.dim() != 2:
         raise ValueError(f"{what} is [T, H]")
     code = _row_dtype(what, x)
-    _check(what, x, x.shape, x.dtype, x.device)
+    _check_contiguous(what, x)
     return x.shape[0], x.shape[1], x.device, code
 
 
@@ -999,10 +1030,13 @@ def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Op
     if residual is not None:
         _check("residual", residual, (T, H), x.dtype, dev)
     r = _check_rng(p, rng, dev)
-    with _launch(dev, stream) as raw:
-        y = torch.empty_like(x)
-        _ok(_lib.moe_dropout_fwd(T, H, code, x.data_ptr(), None if residual is None else residual.data_ptr(), p, r,
-                                 y.data_ptr(), raw), "moe_dropout_fwd")
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return dropout(x, p, rng, residual)
+    y = torch.empty_like(x)
+    _ok(_lib.moe_dropout_fwd(T, H, code, x.data_ptr(), None if residual is None else residual.data_ptr(), p, r,
+                             y.data_ptr(), raw), "moe_dropout_fwd")
     return y
 
 
@@ -1011,7 +1045,10 @@ def dropout_bwd(grad_y: torch.Tensor, p: float, rng: Optional[torch.Tensor], str
     _explicit_grad("dropout", grad_y)
     T, H, dev, code = _check_hidden("grad_y", grad_y)
     r = _check_rng(p, rng, dev)
-    with _launch(dev, stream) as raw:
-        gx = torch.empty_like(grad_y)
-        _ok(_lib.moe_dropout_bwd(T, H, code, grad_y.data_ptr(), p, r, gx.data_ptr(), raw), "moe_dropout_bwd")
+    raw = _here(dev, stream)
+    if raw is None:
+        with _launch(dev, stream):
+            return dropout_bwd(grad_y, p, rng)
+    gx = torch.empty_like(grad_y)
+    _ok(_lib.moe_dropout_bwd(T, H, code, grad_y.data_ptr(), p, r, gx.data_ptr(), raw), "moe_dropout_bwd")
     return gx

@@ -230,11 +230,11 @@ inline int warps_across(int spans)
 // to kernel, as measured there. -1 on an error.
 inline long long dynamic_grid(const void* kernel, long long units, int waves)
 {
-    const int resident = persistent_grid(kernel, kRowsThreads, 0, units, false);
-    if (resident < 1) return resident;
-    if (waves == 0 || units < 3ll * resident) return persistent_grid(kernel, kRowsThreads, 0, units, true);
-    const long long each = std::max<long long>(1, units / (static_cast<long long>(resident) * waves));
-    return (units + each - 1) / each;
+    const long long resident = persistent_grid(kernel, kRowsThreads, 0, units, false);
+    if (resident < 1) return -1;
+    const long long each = waves == 0 || units < 3 * resident ? (units + resident - 1) / resident
+                                                              : std::max(1ll, units / (resident * waves));
+    return units < 1 ? 1 : (units + each - 1) / each;
 }
 
 // A grid of (row groups, span groups) for CTAs that take 2^wc spans of 8 >> wc rows at a time; x is 0 on an error.
