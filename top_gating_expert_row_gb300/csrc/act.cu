@@ -175,13 +175,14 @@ __global__ void __launch_bounds__(kRowsThreads, dropout_ctas(VEC && !RES)) k_dro
 
 // ---- host --------------------------------------------------------------------
 
-// Launches a kernel whose warps take a row and a span at a time.
+// Launches a kernel whose warps take a row and a span at a time, in three waves (32768 x 1024 GELU 39.7 us against 40.3
+// with one, 16384 x 1001 28.9 against 30.0, its dropout 25.7 against 27.3; six waves 40.9, 32.5 and 27.1).
 template <typename Args>
 int launch_spans(void (*kernel)(Args), Args a, long long rows, cudaStream_t st)
 {
     const int spans = spans_of(a.W);
     a.wc = warps_across(spans);
-    const dim3 grid = span_grid(reinterpret_cast<const void*>(kernel), rows, spans, a.wc, 0);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(kernel), rows, spans, a.wc, 3);
     if (grid.x < 1) return MR_ECUDA;
     return launch_kernel(kernel, grid, dim3(kRowsThreads), 0, st, 0, a) == cudaSuccess ? MR_OK : MR_ECUDA;
 }

@@ -30,8 +30,9 @@ struct PermuteArgs {
 
 // A warp copies 32 * N words of a row, all of its loads in flight before the first store, the next row's id behind them.
 // Bound by the writes: rows are evicted first, which leaves L2 to x, whose rows are read topk times (8192 tokens, 64
-// experts, topk 8, 2048 columns in bf16: 62 us instead of 68), and handed out in six waves of CTAs, since memory serves
-// some SMs faster than others (51 us, 6.1 TB/s; each SM an equal share 62, a CTA for every few rows 61).
+// experts, topk 8, 2048 columns in bf16: 62 us instead of 68), and handed out in eight waves of CTAs, since memory
+// serves some SMs faster than others (51 us, 6.1 TB/s; two waves 58, each SM an equal share 62, a CTA for every few rows
+// 61).
 template <typename Word, int N>
 __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant__ PermuteArgs a)
 {
@@ -94,11 +95,18 @@ struct CombineArgs {
     int T, topk, n_rows, W, wc;
 };
 
-// A warp sums a span of a token: the rows' numbers and weights a lane each, then the rows eight at a time.
+// A warp sums a span of a token: the rows' numbers and weights a lane each, then the rows four at a time. Bound by memory
+// and, behind it, by the loads in flight: five CTAs an SM with four rows a warp (8192 tokens, topk 8, 2048 columns in bf16
+// with dropout and residual: 54.5 us, 6.2 TB/s) do better than three with eight (57.8) or six that spill (55.9), and four
+// waves than one where topk is small (4096 tokens, topk 4: 13.4 us against 14.1, 16.7 with eight rows). fp32 rows take 32
+// bytes a lane and are best left alone, in one wave (8192 tokens, topk 2, 4096 columns: 68.8 us, 5.9 TB/s; three 70.8).
+template <typename T, bool VEC>
+constexpr int combine_ctas() { return sizeof(T) == 2 && VEC ? 5 : 0; }  // 0: the compiler's choice
+
 template <typename T, bool VEC, bool DROP>
-__global__ void __launch_bounds__(kRowsThreads) k_combine(const __grid_constant__ CombineArgs a)
+__global__ void __launch_bounds__(kRowsThreads, combine_ctas<T, VEC>()) k_combine(const __grid_constant__ CombineArgs a)
 {
-    constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;
+    constexpr int kBatch = 4;
     pdl_trigger_small();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -349,7 +357,7 @@ int permute(PermuteArgs a, size_t row_bytes, cudaStream_t st)
     a.words = static_cast<int>(row_bytes / sizeof(Word));
     const int spans = (a.words + 32 * N - 1) / (32 * N);
     a.wc = warps_across(spans);
-    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_permute<Word, N>), a.n_rows, spans, a.wc, 6);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_permute<Word, N>), a.n_rows, spans, a.wc, 8);
     if (grid.x < 1) return MR_ECUDA;
     const int e = launch_kernel(k_permute<Word, N>, grid, dim3(kRowsThreads), 0, st, 0, a);
     return e == cudaSuccess ? MR_OK : MR_ECUDA;
@@ -360,7 +368,7 @@ int combine(CombineArgs a, cudaStream_t st)
 {
     const int spans = spans_of(a.W);
     a.wc = warps_across(spans);
-    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_combine<T, VEC, DROP>), a.T, spans, a.wc, 0);
+    const dim3 grid = span_grid(reinterpret_cast<const void*>(k_combine<T, VEC, DROP>), a.T, spans, a.wc, sizeof(T) == 2 ? 4 : 0);
     if (grid.x < 1) return MR_ECUDA;
     const int e = launch_kernel(k_combine<T, VEC, DROP>, grid, dim3(kRowsThreads), 0, st, 0, a);
     return e == cudaSuccess ? MR_OK : MR_ECUDA;
@@ -391,7 +399,7 @@ int combine_bwd(CombineBwdArgs a, cudaStream_t st)
             const auto kernel = k_combine_bwd_tokens<T, VEC>;
             a.wc = std::min(warps_across(spans_of(a.W)), kTokenWarpsLog2);
             const int tall = warps >> a.wc;
-            const long long g = dynamic_grid(reinterpret_cast<const void*>(kernel), (a.T + tall - 1) / tall, 6);
+            const long long g = dynamic_grid(reinterpret_cast<const void*>(kernel), (a.T + tall - 1) / tall, 4);
             if (g < 1) return MR_ECUDA;
             const int e = launch_kernel(kernel, dim3(static_cast<unsigned>(g)), dim3(kRowsThreads), 0, st, 0, a);
             return e == cudaSuccess ? MR_OK : MR_ECUDA;

@@ -225,16 +225,18 @@ inline int warps_across(int spans)
 }
 
 // CTAs for `units` of work. waves 0: no more than are resident, each with the same number of units in turn. Otherwise,
-// where there are units for it, up to about `waves` times as many, handed out as others end, so that SMs that memory
-// serves faster take more. A CTA's start costs too (about 3.6 ns of the GPU's time): which is better differs from kernel
-// to kernel, as measured there. -1 on an error.
+// where there are units for it, `waves` times as many as are resident, handed out as others end, so that SMs that memory
+// serves faster take more (whole waves: a few CTAs behind the last would have the GPU to themselves, which cost up to a
+// quarter of the time). A CTA's start costs too: which is better differs from kernel to kernel, as measured there. -1 on
+// an error.
 inline long long dynamic_grid(const void* kernel, long long units, int waves)
 {
     const long long resident = persistent_grid(kernel, kRowsThreads, 0, units, false);
     if (resident < 1) return -1;
-    const long long each = waves == 0 || units < 3 * resident ? (units + resident - 1) / resident
-                                                              : std::max(1ll, units / (resident * waves));
-    return units < 1 ? 1 : (units + each - 1) / each;
+    if (units < 1) return 1;
+    if (waves > 0 && units >= resident * waves) return resident * waves;
+    const long long each = (units + resident - 1) / resident;
+    return (units + each - 1) / each;
 }
 
 // A grid of (row groups, span groups) for CTAs that take 2^wc spans of 8 >> wc rows at a time; x is 0 on an error.
