@@ -120,6 +120,35 @@ __device__ __forceinline__ void load_span(const T* row, int c0, int W, int lane,
     }
 }
 
+// Aligned rows through shared memory: a thread asks for its eight elements of rows ahead without holding registers for
+// them, and takes them up itself (so no barrier). N tensors, D rows; at most D - 1 of them are on their way, so that a
+// place is asked for again one row after it was read.
+template <typename T, int N, int D>
+struct Ring {
+    static constexpr int kWords = sizeof(T) / 2;  // of 16 bytes
+    uint4 place[D][N * kWords][kRowsThreads];
+
+    __device__ __forceinline__ void ask(int stage, int tensor, const T* p)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&place[stage][tensor * kWords + i][threadIdx.x]));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p + i * (8 / kWords)) : "memory");
+        }
+    }
+    __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // the oldest of D - 1 rows asked for has arrived
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory"); }
+    __device__ __forceinline__ void take(int stage, int tensor, Pack<T>& q) const
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const uint4 v = place[stage][tensor * kWords + i][threadIdx.x];
+            q.w[4 * i] = v.x; q.w[4 * i + 1] = v.y; q.w[4 * i + 2] = v.z; q.w[4 * i + 3] = v.w;
+        }
+    }
+};
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void store_span(T* row, int c0, int W, int lane, const Pack<T>& q)
 {
