@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_act(const __grid_constant__ Ac
                     // a dropped element is 0 whatever it held
                     const bool kept = !DROP || m[e] != 0.0f;
                     const float d = kept ? m[e] * pd.get(e) : 0.0f;
-                    v[e] = kept ? m[e] * act * u : 0.0f;
+                    v[e] = kept ? act * u * m[e] : 0.0f;  // in the forward's order: the same bits
                     gq[e] = kept ? d * act : 0.0f;
                     gg[e] = kept ? d * u * da : 0.0f;
                 }
