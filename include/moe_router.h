@@ -402,8 +402,9 @@ typedef struct {
 
 /*
  * moe_permute_fwd -- rows[r] = x[sorted_token_ids[r] / topk] for the rows in use, 0 at padding rows (any id outside
- * [0, T*topk)); pair_row [T x topk] (int32): the row of each pair, -1 where topk_idx is outside [0, E_tot) (the pairs
- * that moe_sort drops). topk_idx, sorted_token_ids (n_rows entries) and num_tokens_post_pad are moe_sort's.
+ * [0, T*topk)); pair_row [T x topk] (int32): the row of each pair, -1 for pairs without one: topk_idx outside [0, E_tot)
+ * (moe_sort drops them), or none of the rows in use has the pair's id. What pair_row held before does not matter.
+ * topk_idx, sorted_token_ids (n_rows entries) and num_tokens_post_pad are moe_sort's.
  * *status is raised to MR_ERANGE where num_tokens_post_pad exceeds n_rows (the rows behind are left out) or an id is
  * outside [0, T*topk].
  * moe_permute_bwd -- grad_x[t] = sum_j grad_rows[pair_row[t][j]], pairs of -1 left out.

@@ -3,7 +3,7 @@
 //   rows[r(t,j)] = x[t], 0 at the sort's padding                 (permute; its gradient sums a token's rows)
 //   out[t] = residual[t] + m[t] * sum_j w[t,j] rows[r(t,j)]      (combine; m: dropout's factors, see rows.cuh)
 //   g = m[t] grad_out[t]:  grad_rows[r(t,j)] = w[t,j] g,  grad_w[t,j] = <g, rows[r(t,j)]>
-// All are bound by memory. A token's slots are summed in slot order in fp32 and rounded once: no atomics, the same
+// All are bound by memory. A token's slots are summed in slot order in fp32 and rounded once: no atomic sums, the same
 // bits each time.
 #include <algorithm>
 #include <climits>
@@ -28,6 +28,22 @@ struct PermuteArgs {
     int wc;
 };
 
+__device__ __forceinline__ int load_relaxed(const int32_t* p)
+{
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_relaxed(int32_t* p, int v)
+{
+    asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// A row writes its number to its pair's entry of pair_row; a pair that no row holds (the sort dropped it, its row lies
+// behind the buffer, its id is missing) gets -1 without a pass before this one: what its entry held before, whatever that
+// is, stands only where the row of that number holds the pair, and is exchanged for -1 otherwise, unless the row's own
+// number has come in meanwhile.
+//
 // A warp copies 32 * N words of a row, all of its loads in flight before the first store, the next row's id behind them.
 // Bound by the writes: rows are evicted first, which leaves L2 to x, whose rows are read topk times (8192 tokens, 64
 // experts, topk 8, 2048 columns in bf16: 62 us instead of 68), and handed out in eight waves of CTAs, since memory
@@ -41,22 +57,31 @@ __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant_
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int across = 1 << a.wc, tall = (kRowsThreads / 32) >> a.wc;
     const int first = (static_cast<int>(blockIdx.y) * across + (warp & (across - 1))) * 32 * N;
-    if (blockIdx.y == 0) {
-        for (long long i = static_cast<long long>(blockIdx.x) * kRowsThreads + threadIdx.x; i < a.P;
-             i += static_cast<long long>(gridDim.x) * kRowsThreads) {
-            const int e = __ldcg(a.topk_idx + i);
-            if (e < 0 || e >= a.E_tot) a.pair_row[i] = -1;
-        }
-    }
+    const long long pairs_step = static_cast<long long>(gridDim.x) * kRowsThreads;
+    long long pair = static_cast<long long>(blockIdx.x) * kRowsThreads + threadIdx.x;
+    int expert = 0, was = -1;
+    auto look = [&] {
+        if (blockIdx.y != 0 || pair >= a.P) return false;
+        expert = __ldcg(a.topk_idx + pair);
+        was = load_relaxed(a.pair_row + pair);
+        return true;
+    };
+    bool mine = look();
     int rows = __ldcg(a.npp);
     if (rows > a.n_rows) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_status(a.status, kStatusRange);
         rows = a.n_rows;
     }
-    if (first >= a.words) return;
     const long long step = static_cast<long long>(gridDim.x) * tall;
     long long r = static_cast<long long>(blockIdx.x) * tall + (warp >> a.wc);
     int next = r < rows ? __ldcg(a.ids + r) : 0;
+    while (mine) {
+        if (expert < 0 || expert >= a.E_tot) store_relaxed(a.pair_row + pair, -1);
+        else if (was != -1 && (was < 0 || was >= rows || __ldcg(a.ids + was) != pair)) atomicCAS(a.pair_row + pair, was, -1);
+        pair += pairs_step;
+        mine = look();
+    }
+    if (first >= a.words) return;
     for (; r < rows; r += step) {
         const int id = next;
         if (r + step < rows) next = __ldcg(a.ids + r + step);
@@ -76,7 +101,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant_
             if (c < a.words) __stcs(dst + c, v[i]);
         }
         if (first == 0 && lane == 0) {
-            if (real) a.pair_row[id] = static_cast<int32_t>(r);
+            if (real) store_relaxed(a.pair_row + id, static_cast<int32_t>(r));
             else if (id != a.P) report_status(a.status, kStatusRange);
         }
     }
