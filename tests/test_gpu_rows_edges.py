@@ -82,3 +82,36 @@ def test_pairs_without_a_row(mr, T, k, E, H, block, dropped, missing):
     want_grad = torch.zeros(n_rows, H)
     want_grad[want[want >= 0].long()] = (x[:, None] * w[:, :, None]).view(P, H)[want >= 0]
     assert torch.equal(back["grad_rows"].cpu(), want_grad)
+
+
+def test_as_many_rows_as_the_type_counts(mr):
+    """n_rows = 2^31 - 1, the most that is accepted, all of them in use: one column, so 4 GB a buffer."""
+    n, dev, i32 = (1 << 31) - 1, "cuda", torch.int32
+    T, k = 1400, 3  # with dropout a token's rows share its factors from 4096 pairs on
+    P = T * k
+    at = torch.randperm(n // 1000, generator=torch.Generator().manual_seed(1))[:P] * 999
+    at[:3] = torch.tensor([n - 1, n - 33, 0])  # the last row among them
+    assert at.unique().numel() == P
+    at = at.to(dev)
+    ids = torch.full((n,), P, dtype=i32, device=dev)
+    ids[at] = torch.arange(P, dtype=i32, device=dev)
+    npp = torch.tensor([n], dtype=i32, device=dev)
+    pair_row = at.view(T, k).to(i32)
+    rows = torch.zeros(n, 1, dtype=BF16, device=dev)
+    vals = torch.randn(P, 1, device=dev).to(BF16)
+    rows[at] = vals
+    w, x = torch.rand(T, k, device=dev), torch.randn(T, 1, device=dev).to(BF16)
+    rng = torch.tensor([5, 6], device=dev)
+    padding = torch.ones(n, dtype=torch.bool, device=dev)
+    padding[at] = False
+    for p in (0.0, 0.5):
+        grad = torch.full((n, 1), float("nan"), dtype=BF16, device=dev)
+        got = mr.combine_bwd(x, rows, pair_row, w, ids, npp, p=p, rng=rng, grad_rows=grad)
+        g = x.float() * ref.factors(T, 1, p, rng.tolist()).float().to(dev)
+        assert torch.equal(got["grad_w"], g * vals.view(T, k).float())  # one product in fp32
+        assert torch.equal(grad[at], (g * w).view(P, 1).to(BF16))
+        assert int(torch.count_nonzero(grad.view(torch.int16)[:, 0][padding])) == 0
+    got = mr.permute(x, torch.zeros(T, k, dtype=i32, device=dev), 1, ids, npp, rows=grad)
+    assert torch.equal(got["pair_row"], pair_row)
+    assert torch.equal(grad[at], x.expand(T, k).reshape(P, 1))
+    assert int(torch.count_nonzero(grad.view(torch.int16)[:, 0][padding])) == 0

@@ -200,7 +200,8 @@ struct CombineBwdArgs {
     float* grad_w;
     int32_t* status;
     DropArgs drop;
-    int T, topk, n_rows, W, wc, pad_span;
+    int T, topk, n_rows, W, wc;
+    int pad_span, pads;  // sorted positions of a share, shares
 };
 
 // Zeroes the padding rows among the sorted positions from u * pad_span on, pad_span of them (at most 32).
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_combine_bwd_pairs(const __grid
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const long long P = static_cast<long long>(a.T) * a.topk, warps = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
-    const long long units = P + (a.n_rows + a.pad_span - 1) / a.pad_span;
+    const long long units = P + a.pads;
     DropState ds;
     if constexpr (DROP) ds = drop_state(a.drop);
     for (long long u = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
@@ -360,8 +361,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_combine_bwd_tokens(const __gri
             if (mine == 0 && t < a.T && lane < KB && j0 + lane < a.topk) a.grad_w[t * a.topk + j0 + lane] = sum;
         }
     }
-    const long long units = (a.n_rows + a.pad_span - 1) / a.pad_span, warps = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
-    for (long long u = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + warp; u < units; u += warps)
+    const long long warps = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
+    for (long long u = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + warp; u < a.pads; u += warps)
         zero_padding<VEC, T>(a, u, lane);
 }
 
@@ -416,7 +417,7 @@ int combine_bwd(CombineBwdArgs a, cudaStream_t st)
     // a warp's share of the padding: small layouts are mostly padding and want all SMs for it (64 tokens, 256 experts,
     // blocks of 16: 5.4 us against 16 with 32 rows a warp), in large ones looking for it is what costs
     a.pad_span = a.n_rows <= 32768 ? 4 : 32;
-    const long long pads = (a.n_rows + a.pad_span - 1) / a.pad_span;
+    a.pads = static_cast<int>((static_cast<long long>(a.n_rows) + a.pad_span - 1) / a.pad_span);  // n_rows may be INT_MAX
     if constexpr (DROP) {
         // T=1024 H=2048: topk 4 12.3 us against 12.8 pair by pair, topk 1 10.1 against 7.6; T=512: topk 4 9.5 against 8.3,
         // topk 8 15.0 against 14.6
@@ -431,7 +432,7 @@ int combine_bwd(CombineBwdArgs a, cudaStream_t st)
         }
     }
     const auto kernel = k_combine_bwd_pairs<T, VEC, DROP>;
-    const int g = persistent_grid(reinterpret_cast<const void*>(kernel), kRowsThreads, 0, (pairs + pads + warps - 1) / warps, true);
+    const int g = persistent_grid(reinterpret_cast<const void*>(kernel), kRowsThreads, 0, (pairs + a.pads + warps - 1) / warps, true);
     if (g < 1) return MR_ECUDA;
     const int e = launch_kernel(kernel, dim3(g), dim3(kRowsThreads), 0, st, 0, a);
     return e == cudaSuccess ? MR_OK : MR_ECUDA;
@@ -530,7 +531,7 @@ int moe_combine_bwd(const mr_rows_params* p, const void* grad_out, const void* r
         !at_multiple(grad_w, 4) || !at_multiple(status, 4))
         return MR_EINVAL;
     const CombineBwdArgs a = {grad_out, rows, pair_row, topk_w, sorted_token_ids, num_tokens_post_pad, grad_rows, grad_w,
-                              status, drop, p->T, p->topk, p->n_rows, p->H, 0, 0};
+                              status, drop, p->T, p->topk, p->n_rows, p->H, 0, 0, 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return p->dtype == MR_F32 ? combine_bwd_of<float>(a, st) : combine_bwd_of<__nv_bfloat16>(a, st);
 }
