@@ -19,6 +19,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoerouter.so")
@@ -572,13 +573,22 @@ def aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor, T: in
 
 # ------------------------------------------------------------------- the layer behind the router
 # Serving operators: they have no backward pass, so inputs that ask for a gradient are refused instead of giving
-# results that are cut off from them (under torch.no_grad(), as in serving, they are taken).
+# results that are cut off from them (under torch.no_grad(), as in serving, they are taken), and so are dual tensors.
 
 
 def _forward_only(*tensors) -> None:
     for t in tensors:
         if t is not None and t.requires_grad and torch.is_grad_enabled():
             raise ValueError("this operator has no backward pass: call it under torch.no_grad(), or detach its inputs")
+    _no_tangents(tensors)
+
+
+def _no_tangents(tensors) -> None:
+    """Refuses dual tensors, whose tangents the call would lose; looks at them only inside a dual level."""
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("this call has no forward-mode derivative: detach its inputs")
 
 
 def _check(what: str, t: torch.Tensor, shape, dtype, device) -> None:
@@ -786,7 +796,7 @@ def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = N
 
 # ------------------------------------------------------------------- rows by expert and back
 # Each step and its gradient are calls of their own, as route() and route_bwd() are: inputs that ask autograd for a
-# gradient are refused instead of giving results that are cut off from them. Buffers may be passed in (a training loop
+# gradient, in either mode, are refused instead of giving results that are cut off from them. Buffers may be passed in (a training loop
 # keeps its own); rows behind num_tokens_post_pad are left as they are in those, and undefined in fresh ones.
 
 
@@ -794,6 +804,7 @@ def _explicit_grad(bwd: str, *tensors) -> None:
     for t in tensors:
         if t is not None and t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"gradients are computed by {bwd}(): call this under torch.no_grad(), or detach its inputs")
+    _no_tangents(tensors)
 
 
 def _here(device, stream) -> Optional[int]:
