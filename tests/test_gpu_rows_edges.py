@@ -115,3 +115,51 @@ def test_as_many_rows_as_the_type_counts(mr):
     assert torch.equal(got["pair_row"], pair_row)
     assert torch.equal(grad[at], x.expand(T, k).reshape(P, 1))
     assert int(torch.count_nonzero(grad.view(torch.int16)[:, 0][padding])) == 0
+
+
+@pytest.mark.parametrize("up", [1.0, 2.0 ** 60])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("kind", [0, 1], ids=["silu", "gelu"])
+def test_far_gates_keep_their_values(mr, kind, dtype, up):
+    """Gates so low that the exponentials are subnormal, as long as there is anything left of the results in their type.
+
+    Relative errors as for other gates: an exponential's argument and its rounded square (GELU: 1.5 g^2 EPS, with the
+    polynomial 2 g^2), some EPS besides. fp32: exponents to 150 are kept, so that less than |g| 2^-150 of a result is lost;
+    GELU's products with the exponential are rounded to half a subnormal step, 2^-150, before they are multiplied by g, and
+    its polynomial, taken at 14 for gates beyond, is 0.2 of such a step off: (2 |g| + 4) 2^-150 in all. bf16: exponents to
+    142 are kept, |g| + 1 is below 100 there, and less than 2^-135 of act and act' is lost (half of bf16's least number
+    is 2^-134). Results may be subnormal in their own type.
+    """
+    lo, hi = ((-112.0, -80.0), (-14.5, -12.0))[kind]
+    g = torch.linspace(lo, hi, 64 * 512).view(64, 512).to(dtype)
+    d = g.double()
+    a, da = ref.act(d, kind)
+    flat = (2 * d.abs() + 4) * 2.0 ** -150 + (2.0 ** -135 if dtype is BF16 else 0.0)
+    if kind == 0:
+        rel = (d.abs() + 12) * EPS
+        ta = rel * a.abs() + flat
+        tda = (rel + 3 * EPS) * (a.abs() + torch.sigmoid(d)) + flat
+    else:
+        pdf = torch.exp(-0.5 * d * d) * (2 * torch.pi) ** -0.5
+        rel = (2 * d * d + 10) * EPS
+        ta = rel * a.abs() + flat
+        tda = rel * (a / d).abs() + (1.5 * d * d + 10) * EPS * (d * pdf).abs() + flat
+    step = {F32: 2.0 ** -150, BF16: 2.0 ** -134}[dtype]
+    half = torch.finfo(dtype).eps / 2 * (1 + 2.0 ** -7)  # of the value before it was rounded
+    gu = torch.cat([g, torch.full_like(g, up)], 1).cuda()
+    h = mr.expert_act(gu, act=kind).cpu().double()
+    assert ((h - a * up).abs() <= up * (ta + 2 * EPS * a.abs()) + half * (a * up).abs() + step).all()
+    out = mr.expert_act_bwd(torch.ones_like(g).cuda(), gu, act=kind)
+    got = out["grad_gu"].cpu().double()
+    assert ((got[:, 512:] - a).abs() <= ta + EPS * a.abs() + half * a.abs() + step).all()
+    assert ((got[:, :512] - up * da).abs() <= up * (tda + 2 * EPS * da.abs()) + half * (up * da).abs() + step).all()
+    assert torch.equal(out["h"].cpu().double(), h)
+
+
+def test_far_gates_that_leave_nothing(mr):
+    """Where nothing is left results are 0, not NaN; a NaN stays one."""
+    g = torch.tensor([[-200.0, -1e4, -1e30, -3.4e38, float("nan"), -1.0, 1e30, 0.0]], device="cuda")
+    for kind in (0, 1):
+        gu = torch.cat([g, torch.ones_like(g)], 1)
+        for t in (mr.expert_act(gu, act=kind), mr.expert_act_bwd(torch.ones_like(g), gu, act=kind)["grad_gu"][:, :8]):
+            assert (t[0, :4] == 0).all() and t[0, 4].isnan() and t[0, 5:].isfinite().all(), (kind, t)

@@ -20,36 +20,72 @@ __device__ __forceinline__ float rcp_hw(float x)
     return y;
 }
 
-// act(g) and act'(g) in fp32. The sigmoid is a hardware exponential (of the two-part product, exp_value) and
-// reciprocal: 1 to 2 units of the last place. Phi(-a) = exp(-a^2 / 2) R(s), s = a / (4 + a): R, half the scaled
-// complementary error function of a / sqrt 2, is smooth in s, and a polynomial of degree 9 fitted here by least squares
-// that are weighted again until the errors level (Lawson's method) is within 2^-26 of it, relative, for a up to 14,
-// where the exponential is 0. Near a = 0 an error of s counts little, and behind it R's grows no faster than the
-// exponential's, so Phi keeps its bits for g below zero. Phi(a) = 1 - Phi(-a).
+// act(g) and act'(g) in fp32, for outputs of type T. The sigmoid is a hardware exponential and reciprocal. Phi(-a) =
+// exp(-a^2 / 2) R(s), s = a / (4 + a): R, half the scaled complementary error function of a / sqrt 2, is smooth in s and
+// is a polynomial of degree 9, fitted here by least squares that are weighted again until the errors level (Lawson's
+// method), for a up to 14. Near a = 0 an error of s counts little, and behind it R's grows no faster than the
+// exponential's. Phi(a) = 1 - Phi(-a).
+// Errors: the exponential's argument is rounded, so they grow with it: at most (|g| + 12) 2^-24 of SiLU (tens of units of
+// the last place at g = -80) and (2 g^2 + 10) 2^-24 of GELU's negative side (1e-5 at -13), relative.
+// exp g and exp(-g^2 / 2) become subnormal, which the fast forms flush to 0, while act and act' are still normal numbers.
+// So the exponent is moved by kShift where it matters, and the result moved back by a product: in fp32, where exponents of
+// 100 and more are met (far is 0 or 1, a saturated product: exponents there are multiples of 2^-17), which gives all that
+// fp32 holds; in bf16 always, in one product with log2 e, since the roundings of 2^-20 that this costs are far below
+// bf16's, and g times 2^-16 is exact for bf16's subnormal numbers too. There act is 0 below 2^-135, which bf16 cannot
+// hold.
 // Two values at a time, in packed instructions where there are any (each half rounds as the single one does).
-template <int ACT, bool GRAD>
+template <typename T, int ACT, bool GRAD>
 __device__ __forceinline__ float2 gate(float2 g, float2& da)
 {
-    const float2 one = make_float2(1.0f, 1.0f);
+    constexpr bool kShort = sizeof(T) == 2;
+    auto both = [](float v) { return make_float2(v, v); };
+    auto ex2 = [](float2 v) { return make_float2(exp2_hw(v.x), exp2_hw(v.y)); };
+    auto rcp = [](float2 v) { return make_float2(rcp_hw(v.x), rcp_hw(v.y)); };
+    constexpr float kShift = kShort ? 16.0f : 24.0f, kBack = kShort ? 0x1p-16f : 0x1p-24f;
+    const float2 one = both(1.0f);
+    // fp32: x log2 e, moved towards 0 by kShift where it is beyond 100, and what moves the result back
+    auto exponent = [&](float2 x, float sign, float2& back) {
+        const float2 y = __ffma2_rn(x, both(kLog2eHi), __fmul2_rn(x, both(kLog2eLo)));
+        auto beyond = [&](float v) { return __saturatef(fmaf(v, sign * 0x1p20f, -100.0f * 0x1p20f)); };
+        const float2 far = make_float2(beyond(y.x), beyond(y.y));
+        back = __ffma2_rn(far, both(kBack - 1.0f), one);
+        return __ffma2_rn(far, both(-sign * kShift), y);
+    };
     if constexpr (ACT == MR_SILU) {
-        const float2 d = __fadd2_rn(one, exp_value2(make_float2(-g.x, -g.y)));
-        const float2 s = make_float2(rcp_hw(d.x), rcp_hw(d.y)), a = __fmul2_rn(g, s);
+        float2 a, s;
+        if constexpr (kShort) {
+            const float2 r = rcp(__fadd2_rn(both(kBack), ex2(__ffma2_rn(g, both(-kLog2eHi), both(-kShift)))));
+            a = __fmul2_rn(__fmul2_rn(g, both(kBack)), r);
+            s = __fmul2_rn(r, both(kBack));
+        } else {
+            float2 back;
+            const float2 r = rcp(__fadd2_rn(one, ex2(exponent(make_float2(-g.x, -g.y), 1.0f, back))));
+            a = __fmul2_rn(__fmul2_rn(g, r), back);
+            s = __fmul2_rn(r, back);
+        }
         if constexpr (GRAD) da = __ffma2_rn(a, __fadd2_rn(one, make_float2(-s.x, -s.y)), s);
         return a;
     } else {
         constexpr float kR[] = {0.5f, -1.5957679748535156f, 2.4041967391967773f, -2.1061601638793945f, 0.8699361681938171f,
                                 0.10994171351194382f, -0.2098998725414276f, -0.04766450077295303f, 0.10934294760227203f,
                                 -0.03394665941596031f};
-        auto both = [](float v) { return make_float2(v, v); };
+        constexpr float kScale = kShort ? kBack : 1.0f;  // of R and of the density
         const float2 q = __fmul2_rn(both(0.25f), make_float2(fminf(fabsf(g.x), 14.0f), fminf(fabsf(g.y), 14.0f)));
-        const float2 d = __fadd2_rn(one, q), s = __fmul2_rn(q, make_float2(rcp_hw(d.x), rcp_hw(d.y)));
-        const float2 e = exp_value2(__fmul2_rn(__fmul2_rn(both(-0.5f), g), g));
-        float2 t = both(kR[9]);
+        const float2 s = __fmul2_rn(q, rcp(__fadd2_rn(one, q)));
+        float2 e, back = one;
+        if constexpr (kShort) e = ex2(__ffma2_rn(__fmul2_rn(g, g), both(-0.5f * kLog2eHi), both(kShift)));
+        else e = ex2(exponent(__fmul2_rn(__fmul2_rn(both(-0.5f), g), g), -1.0f, back));
+        float2 t = both(kScale * kR[9]);
 #pragma unroll
-        for (int i = 8; i >= 0; --i) t = __ffma2_rn(t, s, both(kR[i]));
+        for (int i = 8; i >= 0; --i) t = __ffma2_rn(t, s, both(kScale * kR[i]));
         t = __fmul2_rn(t, e);
+        if constexpr (!kShort) t = __fmul2_rn(t, back);
         const float2 cdf = make_float2(g.x > 0.0f ? 1.0f - t.x : t.x, g.y > 0.0f ? 1.0f - t.y : t.y);
-        if constexpr (GRAD) da = __ffma2_rn(g, __fmul2_rn(both(0.39894228040143268f), e), cdf);
+        if constexpr (GRAD) {
+            float2 density = __fmul2_rn(both(kScale * 0.39894228040143268f), e);
+            if constexpr (!kShort) density = __fmul2_rn(density, back);
+            da = __ffma2_rn(g, density, cdf);
+        }
         return __fmul2_rn(g, cdf);
     }
 }
@@ -124,7 +160,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_act(const __grid_constant__ Ac
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 float2 da;
-                const float2 act = gate<ACT, false>(make_float2(pg.get(e), pg.get(e + 1)), da);
+                const float2 act = gate<T, ACT, false>(make_float2(pg.get(e), pg.get(e + 1)), da);
                 v[e] = act.x * pu.get(e);
                 v[e + 1] = act.y * pu.get(e + 1);
             }
@@ -140,7 +176,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_act(const __grid_constant__ Ac
 #pragma unroll
             for (int e0 = 0; e0 < 8; e0 += 2) {
                 float2 da2;
-                const float2 act2 = gate<ACT, true>(make_float2(pg.get(e0), pg.get(e0 + 1)), da2);
+                const float2 act2 = gate<T, ACT, true>(make_float2(pg.get(e0), pg.get(e0 + 1)), da2);
 #pragma unroll
                 for (int e = e0; e < e0 + 2; ++e) {
                     const float act = e == e0 ? act2.x : act2.y, da = e == e0 ? da2.x : da2.y, u = pu.get(e);
