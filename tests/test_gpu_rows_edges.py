@@ -163,3 +163,42 @@ def test_far_gates_that_leave_nothing(mr):
         gu = torch.cat([g, torch.ones_like(g)], 1)
         for t in (mr.expert_act(gu, act=kind), mr.expert_act_bwd(torch.ones_like(g), gu, act=kind)["grad_gu"][:, :8]):
             assert (t[0, :4] == 0).all() and t[0, 4].isnan() and t[0, 5:].isfinite().all(), (kind, t)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("T,k,H", [(7, 2, 264), (7, 5, 257), (1400, 3, 520), (1100, 4, 257)])
+def test_dropped_gradients_are_zero_whatever_they_meet(mr, T, k, H, dtype):
+    """A dropped element's gradient is 0 in grad_w's sums and in grad_rows, although the row holds an infinity or NaN there
+    or the weight is one: out does not depend on them. Kept elements follow the formula. Pairs alone and, from 4096 on,
+    tokens whose rows share their factors."""
+    gen = torch.Generator().manual_seed(H + T)
+    P, p, dev = T * k, 0.5, "cuda"
+    pair_row = torch.randperm(P, generator=gen).view(T, k)
+    ids = torch.empty(P, dtype=torch.int32)
+    ids[pair_row.view(-1)] = torch.arange(P, dtype=torch.int32)
+    rng = torch.tensor([21, 22])
+    f = ref.factors(T, H, p, rng.tolist())
+    go = torch.randn(T, H, generator=gen).to(dtype)
+    rows = torch.randn(P, H, generator=gen).to(dtype)
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")]).to(dtype)
+    which = torch.randint(0, 6, (T, k, H), generator=gen)
+    which = torch.where((f == 0)[:, None].expand(T, k, H), which, 5)
+    mine = rows[pair_row]
+    mine = torch.where(which < 3, bad[which.clamp(max=2)], mine)
+    rows[pair_row.view(-1)] = mine.view(P, H)
+    w = torch.rand(T, k, generator=gen)
+    w[0, 0], w[T // 2, 1], w[T - 1, 0] = float("inf"), float("nan"), -float("inf")
+    out = mr.combine_bwd(go.to(dev), rows.to(dev), pair_row.to(torch.int32).to(dev), w.to(dev), ids.to(dev),
+                         torch.tensor([P], dtype=torch.int32, device=dev), p=p, rng=rng.to(dev))
+    g = go.double() * f
+    kept = (f != 0)[:, None].expand(T, k, H)
+    terms = torch.where(kept, g[:, None] * mine.double(), 0.0)
+    assert ((out["grad_w"].cpu().double() - terms.sum(2)).abs()
+            <= ((H + 255) // 256 * 8 + 7) * EPS * terms.abs().sum(2)).all()  # a lane's chain, lanes, the scale
+    want = torch.where(kept, g[:, None] * w.double()[:, :, None], 0.0).view(P, H)
+    got = out["grad_rows"].cpu()[pair_row.view(-1)].double()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+    fine = want.isfinite()
+    assert (got[~fine & ~want.isnan()] == want[~fine & ~want.isnan()]).all()
+    half = torch.finfo(dtype).eps / 2 * (1 + 2.0 ** -7)
+    assert ((got - want).abs()[fine] <= (3 * EPS + half) * want.abs()[fine]).all()  # the scale, two products, the output's

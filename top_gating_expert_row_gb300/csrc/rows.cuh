@@ -215,11 +215,31 @@ __device__ __forceinline__ uint4 philox(const DropState& s, uint32_t block, uint
     return make_uint4(a, b, c, d);
 }
 
+// Ones in the places of a pack whose elements are kept, zeros in the others.
+template <typename T>
+struct Keep {
+    uint32_t w[2 * sizeof(T)];
+    __device__ __forceinline__ void set(int i, bool kept)
+    {
+        if constexpr (sizeof(T) == 4) w[i] = kept ? 0xffffffffu : 0u;
+        else if (i & 1) w[i >> 1] |= kept ? 0xffff0000u : 0u;
+        else w[i >> 1] = kept ? 0x0000ffffu : 0u;
+    }
+    __device__ __forceinline__ void apply(Pack<T>& p) const
+    {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(2 * sizeof(T)); ++i) p.w[i] &= w[i];
+    }
+};
+struct NoKeep {
+    __device__ __forceinline__ void set(int, bool) {}
+};
+
 // v[i] times its factor, for the lane's elements of the span at column c0 of `row`; a dropped element is 0 whatever it
-// held. All 32 lanes take part.
-template <bool VEC>
+// held. All 32 lanes take part. keep: which are kept, for what else meets them.
+template <bool VEC, typename K = NoKeep>
 __device__ __forceinline__ void drop_span(const DropArgs& d, const DropState& s, uint32_t row, int c0, int lane,
-                                          float (&v)[8])
+                                          float (&v)[8], K&& keep = {})
 {
     const uint4 r = philox(s, static_cast<uint32_t>(c0 / 8 + lane), row);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -228,18 +248,30 @@ __device__ __forceinline__ void drop_span(const DropArgs& d, const DropState& s,
         for (int i = 0; i < 8; ++i) {
             const bool kept = ((i & 1) ? w[i >> 1] : w[i >> 1] << 16) > d.above;
             v[i] = kept ? v[i] * d.scale : 0.0f;
+            keep.set(i, kept);
         }
     } else {
         // lane l made block c0 / 8 + l: its eight bits go to the lanes that hold these columns
-        uint32_t keep = 0;
+        uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) keep |= (((i & 1) ? w[i >> 1] : w[i >> 1] << 16) > d.above ? 1u : 0u) << i;
+        for (int i = 0; i < 8; ++i) bits |= (((i & 1) ? w[i >> 1] : w[i >> 1] << 16) > d.above ? 1u : 0u) << i;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t k = __shfl_sync(kFull, keep, 4 * i + (lane >> 3));
-            v[i] = (k >> (lane & 7)) & 1u ? v[i] * d.scale : 0.0f;
+            const uint32_t k = __shfl_sync(kFull, bits, 4 * i + (lane >> 3));
+            const bool kept = (k >> (lane & 7)) & 1u;
+            v[i] = kept ? v[i] * d.scale : 0.0f;
+            keep.set(i, kept);
         }
     }
+}
+
+// The factor of one element.
+__device__ __forceinline__ float drop_factor(const DropArgs& d, const DropState& s, uint32_t row, int column)
+{
+    const uint4 r = philox(s, static_cast<uint32_t>(column / 8), row);
+    const int i = column & 7;
+    const uint32_t w = i < 4 ? (i < 2 ? r.x : r.y) : (i < 6 ? r.z : r.w);
+    return ((i & 1) ? w : w << 16) > d.above ? d.scale : 0.0f;
 }
 
 // How a CTA's 8 warps are laid over (rows, spans): 2^wc spans side by side, the rest on further rows. As many spans
