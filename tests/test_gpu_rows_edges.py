@@ -202,3 +202,36 @@ def test_dropped_gradients_are_zero_whatever_they_meet(mr, T, k, H, dtype):
     assert (got[~fine & ~want.isnan()] == want[~fine & ~want.isnan()]).all()
     half = torch.finfo(dtype).eps / 2 * (1 + 2.0 ** -7)
     assert ((got - want).abs()[fine] <= (3 * EPS + half) * want.abs()[fine]).all()  # the scale, two products, the output's
+
+
+@pytest.mark.parametrize("p", [0.0, 0.5])
+def test_gradients_and_padding_past_32_bits(mr, p):
+    """Pairs and padding rows whose elements lie past 2^31, a gradient of 4.4 GB that holds NaN before; with dropout in the
+    kernel whose tokens share their factors."""
+    n, H, T, k, dev = 270001, 8192, 1400, 3, "cuda"
+    P = T * k
+    gen = torch.Generator().manual_seed(3)
+    at = torch.randperm(n - 1, generator=gen)[:P]
+    at[0] = n - 1
+    assert (at * H >= 1 << 31).sum() > 100
+    at = at.to(dev)
+    ids = torch.full((n,), P, dtype=torch.int32, device=dev)
+    ids[at] = torch.arange(P, dtype=torch.int32, device=dev)
+    rows = torch.full((n, H), float("nan"), dtype=BF16, device=dev)  # the padding is not read
+    vals = torch.randn(P, H, generator=gen).to(BF16).to(dev)
+    rows[at] = vals
+    go, w = torch.randn(T, H, generator=gen).to(BF16).to(dev), torch.rand(T, k, generator=gen).to(dev)
+    rng = torch.tensor([8, 9], device=dev)
+    npp = torch.tensor([n], dtype=torch.int32, device=dev)
+    grad = torch.full((n, H), float("nan"), dtype=BF16, device=dev)
+    got = mr.combine_bwd(go, rows, at.view(T, k).to(torch.int32), w, ids, npp, p=p, rng=rng, grad_rows=grad)
+    g = go.float() * ref.factors(T, H, p, rng.tolist()).float().to(dev)  # factors of 0, 1 and 2: exact
+    assert torch.equal(grad[at], (g[:, None] * w[:, :, None]).to(BF16).view(P, H))
+    terms = g.double()[:, None] * vals.view(T, k, H).double()
+    # a lane's chain, lanes, the four warps of a token
+    assert ((got["grad_w"] - terms.sum(2)).abs() <= (H // 32 + 10) * EPS * terms.abs().sum(2)).all()
+    padding = torch.ones(n, dtype=torch.bool, device=dev)
+    padding[at] = False
+    for first in range(0, n, 30000):
+        part = grad[first : first + 30000].view(torch.int16)
+        assert not (part != 0).any(1)[padding[first : first + 30000]].any(), first
