@@ -425,6 +425,7 @@ int moe_permute_bwd(const mr_rows_params* p, const void* grad_rows, const int32_
  *   grad_rows[pair_row[t][j]] = topk_w[t][j] * g[t], 0 at padding rows;  grad_w[t][j] = <g[t], rows[pair_row[t][j]]>, 0
  *   for pairs without a row. A dropped element's part of both is 0 whatever the weight or the row hold there.
  *   sorted_token_ids and num_tokens_post_pad say which rows are padding.
+ *   moe_router_bwd takes grad_w as dense grad_probs: zeros, and grad_w[t][j] at topk_idx[t][j] for the routed slots j.
  * Errors as above, and MR_EINVAL for a drop_p outside [0, 1] or without the rng it needs.
  */
 int moe_combine_fwd(const mr_rows_params* p, const void* rows, const int32_t* pair_row, const float* topk_w,

@@ -235,3 +235,58 @@ def test_gradients_and_padding_past_32_bits(mr, p):
     for first in range(0, n, 30000):
         part = grad[first : first + 30000].view(torch.int16)
         assert not (part != 0).any(1)[padding[first : first + 30000]].any(), first
+
+
+@pytest.mark.parametrize("score_fn,renorm,shared", [(0, 0, 0), (0, 1, 1), (1, 0, 1), (1, 1, 0)])
+def test_from_logits_to_gradients(mr, score_fn, renorm, shared):
+    """A layer's training pass from the router's logits to their gradient: route, sort, permute, products by torch,
+    expert_act, combine, and back, where combine_bwd's grad_w goes to route_bwd by a scatter into zeros [T, E], the shared
+    experts' columns left out (their weights are constants). Against the whole in 64 bits with the selection held fixed.
+
+    d = 1.5e-3 bounds the error of grad_w as it does in the test of a layer's gradients. A weight's gradient enters ds with
+    scaling / A, once as itself and once in their mean, A > 1/2 being the sum of the winners' scores (or 1): 2 * 1.5 * 2 d;
+    dx = s (ds - sum s ds) doubles that: 12 d.
+    """
+    from test_gpu_rows import _layer
+
+    T, k, E, H, I, block, p, d = 29, 3, 7, 48, 20, 4, 0.25, 1.5e-3
+    gen = torch.Generator().manual_seed(6)
+    x, logits = torch.randn(T, H, generator=gen), torch.randn(T, E, generator=gen)
+    all_e = E + shared
+    w13, w2 = torch.randn(all_e, 2 * I, H, generator=gen) * H ** -0.5, torch.randn(all_e, H, I, generator=gen) * I ** -0.5
+    go, rng = torch.randn(T, H, generator=gen), torch.tensor([[12, 0], [12, 1]])
+    options = dict(score_fn=score_fn, renorm=renorm, n_shared=shared, scaling=1.5, shared_weight=0.5)
+    back = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = False
+    try:
+        r = mr.route(logits.cuda(), k + shared, **options)
+        out, backward, _ = _layer(mr, x.cuda(), r["topk_idx"], r["topk_w"], w13.cuda(), w2.cuda(), rng.cuda(), p, block, 0)
+        got = backward(go.cuda())
+        idx = r["topk_idx"][:, :k].long()
+        grad_probs = torch.zeros(T, E, device="cuda").scatter_(1, idx, got["w"][:, :k])
+        grad_logits = mr.route_bwd(mr.params_for(logits, k + shared, **options), grad_probs, r["intermediate"], r["routing_map"])
+    finally:
+        torch.backends.cuda.matmul.allow_tf32 = back
+
+    idx = r["topk_idx"].cpu()
+    assert (idx[:, k:] == torch.arange(E, all_e)).all()
+    _, n, pair_row = ref.sort(idx, all_e, block)
+    f_row, f_out = ref.factors(n, I, p, rng[0].tolist()), ref.factors(T, H, p, rng[1].tolist())
+    leaf = logits.double().requires_grad_()
+    s = torch.softmax(leaf, 1) if score_fn == 0 else torch.sigmoid(leaf)
+    win = s.gather(1, idx[:, :k].long())
+    total = win.sum(1, keepdim=True)
+    assert not renorm or (total > 0.5).all()
+    w = torch.cat([1.5 * (win / total if renorm else win), torch.full((T, shared), 0.5, dtype=torch.float64)], 1)
+    x64, w13, w2 = x.double(), w13.double(), w2.double()
+    y = torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k + shared):
+            gu = w13[idx[t, j]] @ x64[t]
+            h = f_row[pair_row[t, j]] * ref.act(gu[:I], 0)[0] * gu[I:]
+            y[t] = y[t] + w[t, j] * (w2[idx[t, j]] @ h)
+    want = x64 + f_out * y
+    assert ((out.cpu().double() - want).abs() < d).all()
+    want.backward(go.double())
+    assert ((grad_logits.cpu().double() - leaf.grad).abs() < 12 * d).all()
+    assert leaf.grad.abs().max() > 1

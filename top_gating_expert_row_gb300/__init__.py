@@ -949,7 +949,8 @@ def combine_bwd(grad_out: torch.Tensor, rows: torch.Tensor, pair_row: torch.Tens
                 rng: Optional[torch.Tensor] = None, grad_rows: Optional[torch.Tensor] = None,
                 status: Optional[torch.Tensor] = None, stream=None) -> dict:
     """moe_combine_bwd: grad_rows [n_rows, H] (zeros at padding) and grad_w [T, topk] (fp32) of combine() with the same
-    rows, weights, p and rng. The residual's gradient is grad_out."""
+    rows, weights, p and rng. The residual's gradient is grad_out. route_bwd() takes grad_w scattered into zeros [T, E] by
+    the routed slots of topk_idx."""
     _explicit_grad("combine", grad_out, rows, topk_w, grad_rows)
     T, k, n, H, dev, code = _rows_and_pairs("rows", rows, pair_row)
     _check("grad_out", grad_out, (T, H), rows.dtype, dev)
