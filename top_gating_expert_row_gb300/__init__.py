@@ -667,24 +667,34 @@ def _launch(device, stream):
     return _Launch(device, stream)
 
 
+def _fits(*sizes) -> None:
+    """Refuses sizes that the library's 32-bit fields would wrap, which then pass for small ones."""
+    for n in sizes:
+        if n > 0x7FFFFFFF:
+            raise ValueError(f"sizes go up to 2^31 - 1, got {n}")
+
+
 # The options of a call and the workspace it needs depend on its sizes alone: kept, so that a decode step does not
 # build them again (and nothing else is).
 
 
 @functools.lru_cache(maxsize=1024)
 def _experts_plan(T, H, I, E, topk, act):
+    _fits(T, H, I, E, topk)
     p = mr_expert_params(T, H, I, E, topk, MR_BF16, act)
     return ctypes.byref(p), moe_experts_workspace_bytes(p)
 
 
 @functools.lru_cache(maxsize=1024)
 def _layer_plan(H, I, act, *options):
+    _fits(H, I, *options[:3])
     cp = mr_router_params(*options, None)
     return ctypes.byref(cp), moe_layer_workspace_bytes(cp, H, I, act)
 
 
 @functools.lru_cache(maxsize=1024)
 def _adapter_plan(T, K, N, n, rank, out_f32):
+    _fits(T, K, N, n, rank)
     p = mr_adapter_params(T, K, N, n, rank, MR_BF16, MR_F32 if out_f32 else MR_BF16)
     return ctypes.byref(p), moe_adapter_proj_workspace_bytes(p)
 
@@ -740,6 +750,7 @@ def layer(x: torch.Tensor, logits: torch.Tensor, topk: int, w13: torch.Tensor, w
         p, nb = _layer_plan(H, I, act, *options)
     else:
         _check("bias", bias, (E,), torch.float32, dev)
+        _fits(H, I, *options[:3])
         cp = mr_router_params(*options, bias.data_ptr())
         p, nb = ctypes.byref(cp), moe_layer_workspace_bytes(cp, H, I, act)
     with _launch(dev, stream) as raw:
@@ -843,11 +854,13 @@ def _check_buffer(what: str, t: Optional[torch.Tensor], shape, dtype, device) ->
 
 @functools.lru_cache(maxsize=1024)
 def _rows_plan(T, H, topk, n_rows, dtype):
+    _fits(T, H, topk, n_rows)
     return ctypes.byref(mr_rows_params(T, H, topk, n_rows, dtype))
 
 
 @functools.lru_cache(maxsize=1024)
 def _act_plan(n_rows, I, act, dtype):
+    _fits(n_rows, I)
     return ctypes.byref(mr_act_params(n_rows, I, act, dtype))
 
 
@@ -882,6 +895,7 @@ def permute(x: torch.Tensor, topk_idx: torch.Tensor, E_tot: int, sorted_token_id
     _check("sorted_token_ids", sorted_token_ids, (n,), torch.int32, dev)
     _check("num_tokens_post_pad", num_tokens_post_pad, (1,), torch.int32, dev)
     _check_buffer("rows", rows, (n, H), x.dtype, dev)
+    _fits(E_tot)
     st = _check_status(status, dev)
     raw = _here(dev, stream)
     if raw is None:
@@ -1031,7 +1045,9 @@ def _check_hidden(what: str, x: torch.Tensor):
         raise ValueError(f"{what} is [T, H]")
     code = _row_dtype(what, x)
     _check_contiguous(what, x)
-    return x.shape[0], x.shape[1], x.device, code
+    T, H = x.shape
+    _fits(T, H)
+    return T, H, x.device, code
 
 
 def dropout(x: torch.Tensor, p: float, rng: Optional[torch.Tensor], residual: Optional[torch.Tensor] = None,
