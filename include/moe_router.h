@@ -405,8 +405,8 @@ typedef struct {
  * [0, T*topk)); pair_row [T x topk] (int32): the row of each pair, -1 for pairs without one: topk_idx outside [0, E_tot)
  * (moe_sort drops them), or none of the rows in use has the pair's id. What pair_row held before does not matter.
  * topk_idx, sorted_token_ids (n_rows entries) and num_tokens_post_pad are moe_sort's.
- * *status is raised to MR_ERANGE where num_tokens_post_pad exceeds n_rows (the rows behind are left out) or an id is
- * outside [0, T*topk].
+ * *status is raised to MR_ERANGE where num_tokens_post_pad exceeds n_rows (the rows behind are left out), an id is
+ * outside [0, T*topk], or a row in use has a pair whose topk_idx is outside [0, E_tot) (its pair_row is -1 all the same).
  * moe_permute_bwd -- grad_x[t] = sum_j grad_rows[pair_row[t][j]], pairs of -1 left out.
  * Errors: MR_EINVAL (null or misaligned pointer, T < 0, H, topk or E_tot < 1, n_rows < 0, unknown dtype, T*topk >=
  * INT_MAX), MR_EUNSUPPORTED (H), MR_ECUDA. In this and the calls below a pair_row outside [-1, n_rows) counts as -1 and

@@ -290,3 +290,21 @@ def test_from_logits_to_gradients(mr, score_fn, renorm, shared):
     want.backward(go.double())
     assert ((grad_logits.cpu().double() - leaf.grad).abs() < 12 * d).all()
     assert leaf.grad.abs().max() > 1
+
+
+def test_rows_of_pairs_that_topk_idx_drops(mr):
+    """Sorted for more experts than E_tot says: the pairs beyond have -1 each time, and the status word says so."""
+    T, k, E, H = 3000, 4, 12, 16
+    gen = torch.Generator().manual_seed(4)
+    idx = torch.argsort(torch.rand(T, E, generator=gen), 1)[:, :k].to(torch.int32)
+    srt = mr.sort(idx.cuda(), torch.ones(T, k, device="cuda"), E, 16)
+    ids, n = srt["sorted_token_ids"], srt["num_tokens_post_pad"]
+    _, _, pair_row = ref.sort(idx, E, 16)
+    x = torch.randn(T, H, generator=gen).cuda()
+    for E_tot, code in ((E, 0), (E - 2, mr.MR_ERANGE)):
+        want = torch.where(idx < E_tot, pair_row, -1)
+        for _ in range(4):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = mr.permute(x, idx.cuda(), E_tot, ids, n, status=status)
+            assert torch.equal(out["pair_row"].cpu().long(), want) and int(status) == code
+            assert torch.equal(out["rows"][pair_row.view(-1).cuda()], x.repeat_interleave(k, 0))

@@ -40,7 +40,7 @@ __device__ __forceinline__ void store_relaxed(int32_t* p, int v)
     asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// A row writes its number to its pair's entry of pair_row; a pair that no row holds (the sort dropped it, its row lies
+// A row writes its number to its pair's entry of pair_row, unless topk_idx drops the pair; a pair that no row holds (the sort dropped it, its row lies
 // behind the buffer, its id is missing) gets -1 without a pass before this one: what its entry held before, whatever that
 // is, stands only where the row of that number holds the pair, and is exchanged for -1 otherwise, unless the row's own
 // number has come in meanwhile.
@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant_
         const int id = next;
         if (r + step < rows) next = __ldcg(a.ids + r + step);
         const bool real = id >= 0 && id < a.P;
+        const int of = real && first == 0 && lane == 0 ? __ldcg(a.topk_idx + id) : -1;
         Word v[N];
         const Word* src = static_cast<const Word*>(a.x) + static_cast<long long>(real ? id / a.topk : 0) * a.words;
         Word* dst = static_cast<Word*>(a.rows) + r * a.words;
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_permute(const __grid_constant_
             if (c < a.words) __stcs(dst + c, v[i]);
         }
         if (first == 0 && lane == 0) {
-            if (real) store_relaxed(a.pair_row + id, static_cast<int32_t>(r));
-            else if (id != a.P) report_status(a.status, kStatusRange);
+            if (of >= 0 && of < a.E_tot) store_relaxed(a.pair_row + id, static_cast<int32_t>(r));
+            else if (real || id != a.P) report_status(a.status, kStatusRange);
         }
     }
 }
