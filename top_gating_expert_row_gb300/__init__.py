@@ -807,8 +807,9 @@ def adapter_proj(x: torch.Tensor, w: torch.Tensor, a: Optional[torch.Tensor] = N
 
 # ------------------------------------------------------------------- rows by expert and back
 # Each step and its gradient are calls of their own, as route() and route_bwd() are: inputs that ask autograd for a
-# gradient, in either mode, are refused instead of giving results that are cut off from them. Buffers may be passed in (a training loop
-# keeps its own); rows behind num_tokens_post_pad are left as they are in those, and undefined in fresh ones.
+# gradient, in either mode, are refused instead of giving results that are cut off from them. The buffers of rows
+# (rows, grad_rows, gu's gradient, h) may be passed in, as a training loop keeps its own: rows behind num_tokens_post_pad
+# are left as they are in those, and undefined in fresh ones. pair_row, grad_w and outputs of tokens are made by the call.
 
 
 def _explicit_grad(bwd: str, *tensors) -> None:

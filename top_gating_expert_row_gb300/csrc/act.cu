@@ -5,7 +5,7 @@
 //   d = m * grad_h:  grad_u = d act(g),  grad_g = d u act'(g);  h again where it is asked for
 //   y = residual + m * x;  grad_x = m * grad_y
 //   SiLU: act = g s, act' = s + g s (1 - s), s = 1 / (1 + exp -g);  GELU: act = g Phi(g), act' = Phi(g) + g phi(g)
-// Bound by memory, but for what the generator and erfc cost in bf16.
+// Bound by memory, but for what the generator and the exponentials cost in bf16.
 #include <climits>
 
 #include "rows.cuh"
@@ -101,9 +101,11 @@ struct ActArgs {
 };
 
 // bf16 rows at aligned widths are asked for two ahead through shared memory, which holds what registers would: 30016 of
-// 32768 x 1024 with dropout 31.5 us (5.9 TB/s) against 35.5, GELU 32768 x 1024 33.3 against 40.5, the gradient of 32000 x
-// 2048 120.9 (6.5 TB/s) against 123.7; ahead in registers 37 (fewer warps). fp32 takes twice the shared memory and is
-// slower for it (16384 x 2048 GELU 88 us against 65).
+// 32768 x 1024 with dropout 31.4 us (5.9 TB/s) against 35.7 with loads to registers, GELU 32768 x 1024 32.4 against 36.5,
+// the gradient of 32000 x 2048 with dropout 121.4 (6.5 TB/s) against 123.8, of 8000 x 768 13.0 against 13.7; ahead in
+// registers 37 (fewer warps). A gradient whose warps have few rows each loses by it (2000 x 1024 6.0 us against 5.5; the
+// forward 3.6 against 3.8). fp32 takes twice the shared memory and is slower for it (16384 x 2048 GELU 88 us against 65,
+// its gradient 82 against 64 at half the rows).
 template <typename T, bool VEC, int ACT, bool DROP, bool BWD>
 __global__ void __launch_bounds__(kRowsThreads) k_act(const __grid_constant__ ActArgs a)
 {
@@ -211,9 +213,10 @@ struct DropoutArgs {
 };
 
 // Without a residual a warp has one load of 512 bytes in flight beside the generator's chain of dependent products:
-// what counts is the number of warps, so these kernels keep to 32 registers (16384 x 4096 in bf16: 47 us, 5.7 TB/s,
-// against 51 with 36 to 40; two rows a warp or the next row's load ahead take more registers and 56 to 62). With a
-// residual there are twice the loads a warp, and 40 registers are better (16384 x 2048: 31.5 us, 6.4 TB/s, against 33).
+// what counts is the number of warps, so these kernels keep to 32 registers: bf16 takes 30 by itself (16384 x 4096: 49.4
+// us, 5.4 TB/s), fp32 36 without the limit (16384 x 4096 84.3 us, 6.4 TB/s, against 85.4; 4096 x 1024 8.3 against 7.5). Two
+// rows a warp or the next row's load ahead took more registers and 56 to 62 us in bf16. With a residual there are twice
+// the loads a warp, and the compiler's choice stands (16384 x 2048 in bf16: 31.2 us, 6.5 TB/s).
 constexpr int dropout_ctas(bool few_registers) { return few_registers ? 8 : 0; }  // 0: the compiler's choice
 
 template <typename T, bool VEC, bool DROP, bool RES>
@@ -247,8 +250,9 @@ __global__ void __launch_bounds__(kRowsThreads, dropout_ctas(VEC && !RES)) k_dro
 
 // ---- host --------------------------------------------------------------------
 
-// Launches a kernel whose warps take a row and a span at a time, in three waves (32768 x 1024 GELU 39.7 us against 40.3
-// with one, 16384 x 1001 28.9 against 30.0, its dropout 25.7 against 27.3; six waves 40.9, 32.5 and 27.1).
+// Launches a kernel whose warps take a row and a span at a time, in three waves (with one, with six): 32768 x 1024 GELU
+// 32.2 us (35.0, 33.8), 30016 x 1024 with dropout 31.3 (32.4, 33.1), dropout 16384 x 2048 with residual 31.2 (31.6, 32.6).
+// Not everywhere the best: 16384 x 1001 with dropout 30.5 (29.2, 31.4), dropout 16384 x 1280 20.2 (18.0, 29.9).
 template <typename Args>
 int launch_spans(void (*kernel)(Args), Args a, long long rows, cudaStream_t st)
 {

@@ -124,7 +124,7 @@ struct CombineArgs {
 
 // A warp sums a span of a token: the rows' numbers and weights a lane each, then the rows four at a time. Bound by memory
 // and, behind it, by the loads in flight: five CTAs an SM with four rows a warp (8192 tokens, topk 8, 2048 columns in bf16
-// with dropout and residual: 54.5 us, 6.2 TB/s) do better than three with eight (57.8) or six that spill (55.9), and four
+// with dropout and residual: 54.5 us, 6.2 TB/s) do better than three with eight (57.8) or six (55.9), which spill more (five: 8 bytes, with dropout), and four
 // waves than one where topk is small (4096 tokens, topk 4: 13.4 us against 14.1, 16.7 with eight rows). fp32 rows take 32
 // bytes a lane and are best left alone, in one wave (8192 tokens, topk 2, 4096 columns: 68.8 us, 5.9 TB/s; three 70.8).
 template <typename T, bool VEC>
@@ -320,8 +320,9 @@ __device__ __forceinline__ float pair_again(const CombineBwdArgs& a, long long t
 
 // With dropout: 2^wc warps share a token. Each takes every 2^wc-th span of its gradient, makes the factors there once
 // for kTokenRows of the token's rows at a time, and adds their dot products over its lanes, then the warps' in their
-// order. 8192 tokens, topk 4, 4096 columns in bf16: 97 us (6.4 TB/s) against 113 with the factors made for every pair;
-// eight rows at a time take 110, eight warps a token 100, one 106. Behind the tokens the padding rows.
+// order. 8192 tokens, topk 4, 4096 columns in bf16: 97.7 us (6.4 TB/s) against 127 with the factors made for every pair;
+// where four rows and four warps took 97, eight rows took 110, eight warps a token 100, one 106. Behind the tokens the
+// padding rows.
 constexpr int kTokenRows = 4;
 constexpr int kTokenWarpsLog2 = 2;
 
@@ -456,12 +457,16 @@ int combine_bwd(CombineBwdArgs a, cudaStream_t st)
     const int warps = kRowsThreads / 32;
     const long long pairs = static_cast<long long>(a.T) * a.topk;
     // a warp's share of the padding: small layouts are mostly padding and want all SMs for it (64 tokens, 256 experts,
-    // blocks of 16: 5.4 us against 16 with 32 rows a warp), in large ones looking for it is what costs
+    // topk 8, blocks of 16, H=2048: 5.2 us against 16.1 with 32 rows a warp; 2048 tokens, 64 experts, topk 4, blocks of 64
+    // 16.7 against 18.6), in large ones there is little to do and both do alike (8192 tokens, topk 8, 64 experts 93.0 with
+    // 32, 93.6 with 4). It is the part of padding that counts, not the number of rows: a large layout that is mostly
+    // padding is on the wrong side (512 tokens, 384 experts, topk 8, blocks of 128: 45.0 us, 38.2 with 4)
     a.pad_span = a.n_rows <= 32768 ? 4 : 32;
     a.pads = static_cast<int>((static_cast<long long>(a.n_rows) + a.pad_span - 1) / a.pad_span);  // n_rows may be INT_MAX
     if constexpr (DROP) {
-        // T=1024 H=2048: topk 4 12.3 us against 12.8 pair by pair, topk 1 10.1 against 7.6; T=512: topk 4 9.5 against 8.3,
-        // topk 8 15.0 against 14.6
+        // bf16, H=2048, by tokens (pair by pair): T=1024 topk 4 12.7 us (14.0), T=2048 topk 4 19.4 (24.0); below the rule's
+        // sizes T=1024 topk 1 10.5 (7.8), T=512 topk 4 10.0 (8.6), T=2048 topk 2 15.7 (13.9). At its border pairs are
+        // still better: T=512 topk 8 15.1 (13.8), T=1366 topk 3 15.3 (14.0)
         if (a.topk >= 3 && pairs >= 4096) {
             const auto kernel = k_combine_bwd_tokens<T, VEC>;
             a.wc = std::min(warps_across(spans_of(a.W)), kTokenWarpsLog2);

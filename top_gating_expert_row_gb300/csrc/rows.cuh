@@ -300,7 +300,9 @@ inline long long dynamic_grid(const void* kernel, long long units, int waves)
     return (units + each - 1) / each;
 }
 
-// A grid of (row groups, span groups) for CTAs that take 2^wc spans of 8 >> wc rows at a time; x is 0 on an error.
+// A grid of (row groups, span groups) for CTAs that take 2^wc spans of 8 >> wc rows at a time; x is 0 on an error. Waves
+// are rounded up to whole row groups: where y does not divide the resident CTAs the few behind the last wave cost nothing
+// that could be measured (16384 x 1280, five spans: 20.2 us, 20.1 rounded down).
 inline dim3 span_grid(const void* kernel, long long rows, int spans, int wc, int waves)
 {
     const int tall = (kRowsThreads / 32) >> wc;
