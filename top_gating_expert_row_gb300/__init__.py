@@ -670,7 +670,7 @@ def _launch(device, stream):
 def _fits(*sizes) -> None:
     """Refuses sizes that the library's 32-bit fields would wrap, which then pass for small ones."""
     for n in sizes:
-        if n > 0x7FFFFFFF:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
             raise ValueError(f"sizes go up to 2^31 - 1, got {n}")
 
 

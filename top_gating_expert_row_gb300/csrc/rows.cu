@@ -40,10 +40,10 @@ __device__ __forceinline__ void store_relaxed(int32_t* p, int v)
     asm volatile("st.relaxed.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// A row writes its number to its pair's entry of pair_row, unless topk_idx drops the pair; a pair that no row holds (the sort dropped it, its row lies
-// behind the buffer, its id is missing) gets -1 without a pass before this one: what its entry held before, whatever that
-// is, stands only where the row of that number holds the pair, and is exchanged for -1 otherwise, unless the row's own
-// number has come in meanwhile.
+// A row writes its number to its pair's entry of pair_row, unless topk_idx drops the pair; a pair that no row holds (the
+// sort dropped it, its row lies behind the buffer, its id is missing) gets -1 without a pass before this one: what its
+// entry held before, whatever that is, stands only where the row of that number holds the pair, and is exchanged for -1
+// otherwise, unless the row's own number has come in meanwhile.
 //
 // A warp copies 32 * N words of a row, all of its loads in flight before the first store, the next row's id behind them.
 // Bound by the writes: rows are evicted first, which leaves L2 to x, whose rows are read topk times (8192 tokens, 64
@@ -124,9 +124,10 @@ struct CombineArgs {
 
 // A warp sums a span of a token: the rows' numbers and weights a lane each, then the rows four at a time. Bound by memory
 // and, behind it, by the loads in flight: five CTAs an SM with four rows a warp (8192 tokens, topk 8, 2048 columns in bf16
-// with dropout and residual: 54.5 us, 6.2 TB/s) do better than three with eight (57.8) or six (55.9), which spill more (five: 8 bytes, with dropout), and four
-// waves than one where topk is small (4096 tokens, topk 4: 13.4 us against 14.1, 16.7 with eight rows). fp32 rows take 32
-// bytes a lane and are best left alone, in one wave (8192 tokens, topk 2, 4096 columns: 68.8 us, 5.9 TB/s; three 70.8).
+// with dropout and residual: 54.7 us, 6.1 TB/s) do better than three with eight (57.8) or six (55.9), which spill more
+// (five: 8 bytes, with dropout), and four waves than one where topk is small (4096 tokens, topk 4: 13.4 us against 14.1,
+// 16.7 with eight rows). fp32 rows take 32 bytes a lane and are best left alone, in one wave (8192 tokens, topk 2, 4096
+// columns with dropout: 68.7 us, 5.9 TB/s; three 70.8).
 template <typename T, bool VEC>
 constexpr int combine_ctas() { return sizeof(T) == 2 && VEC ? 5 : 0; }  // 0: the compiler's choice
 
